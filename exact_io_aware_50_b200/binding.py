@@ -19,6 +19,9 @@ FA_ERR_ALIGNMENT = 3
 FA_ERR_ARCH = 4
 FA_ERR_CUDA = 5
 FA_ERR_TIMEOUT = 6
+FA_ERR_PAGE = 7
+
+FA_ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libfa.so")
@@ -29,7 +32,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_pair", "fa_fwd_fp8", "fa_fwd_dropout", "fa_bwd_drop
            "fa_fwd_splitkv_workspace_size", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_prep",
            "fa_bwd_dkdv",
            "fa_bwd_dq", "fa_fwd_f32", "fa_bwd_f32", "fa_device_status", "fa_wait_selftest",
-           "fa_strerror")
+           "fa_rope", "fa_rope_f32", "fa_rope_bwd", "fa_rope_bwd_f32", "fa_rope_freqs",
+           "fa_cache_append", "fa_cache_append_f32", "fa_cache_read", "fa_cache_read_f32",
+           "fa_fwd_cache", "fa_fwd_cache_workspace_size", "fa_strerror")
 
 
 class FaError(RuntimeError):
@@ -79,6 +84,22 @@ def lib():
         L.fa_bwd_dq.restype = I
         L.fa_bwd_workspace_size.argtypes = [I, I, I, I]
         L.fa_bwd_workspace_size.restype = S
+        D = ctypes.c_double
+        for fn in (L.fa_rope, L.fa_rope_f32, L.fa_rope_bwd, L.fa_rope_bwd_f32):
+            fn.argtypes = [P] * 6 + [I] * 8 + [F, P]
+            fn.restype = I
+        L.fa_rope_freqs.argtypes = [P, P, I, D, I, D, I, D, D]
+        L.fa_rope_freqs.restype = I
+        for fn in (L.fa_cache_append, L.fa_cache_append_f32):
+            fn.argtypes = [P] * 9 + [I] * 7 + [P]
+            fn.restype = I
+        for fn in (L.fa_cache_read, L.fa_cache_read_f32):
+            fn.argtypes = [P] * 8 + [I] * 7 + [P]
+            fn.restype = I
+        L.fa_fwd_cache.argtypes = [P] * 10 + [I] * 8 + [F, I, P]
+        L.fa_fwd_cache.restype = I
+        L.fa_fwd_cache_workspace_size.argtypes = [I] * 5
+        L.fa_fwd_cache_workspace_size.restype = S
         L.fa_device_status.argtypes = [P]
         L.fa_device_status.restype = I
         L.fa_wait_selftest.argtypes = [ctypes.c_longlong, P]
@@ -160,6 +181,70 @@ def fa_bwd_dq(ws, dq, B, Hq, Nq, d, scale, stream=0):
 
 def fa_bwd_workspace_size(B, Hq, Nq, d):
     return int(lib().fa_bwd_workspace_size(B, Hq, Nq, d))
+
+
+def fa_rope(q, k, q_out, k_out, positions, freqs, B, Hq, Hkv, N, d, rot_dim, pos_per_batch,
+            interleaved, mscale, stream=0):
+    return lib().fa_rope(q, k, q_out, k_out, positions, freqs, B, Hq, Hkv, N, d, rot_dim,
+                         int(pos_per_batch), int(interleaved), mscale, stream)
+
+
+def fa_rope_f32(q, k, q_out, k_out, positions, freqs, B, Hq, Hkv, N, d, rot_dim, pos_per_batch,
+                interleaved, mscale, stream=0):
+    return lib().fa_rope_f32(q, k, q_out, k_out, positions, freqs, B, Hq, Hkv, N, d, rot_dim,
+                             int(pos_per_batch), int(interleaved), mscale, stream)
+
+
+def fa_rope_bwd(dq_out, dk_out, dq, dk, positions, freqs, B, Hq, Hkv, N, d, rot_dim,
+                pos_per_batch, interleaved, mscale, stream=0):
+    return lib().fa_rope_bwd(dq_out, dk_out, dq, dk, positions, freqs, B, Hq, Hkv, N, d, rot_dim,
+                             int(pos_per_batch), int(interleaved), mscale, stream)
+
+
+def fa_rope_bwd_f32(dq_out, dk_out, dq, dk, positions, freqs, B, Hq, Hkv, N, d, rot_dim,
+                    pos_per_batch, interleaved, mscale, stream=0):
+    return lib().fa_rope_bwd_f32(dq_out, dk_out, dq, dk, positions, freqs, B, Hq, Hkv, N, d,
+                                 rot_dim, int(pos_per_batch), int(interleaved), mscale, stream)
+
+
+def fa_rope_freqs(freqs, mscale, rot_dim, theta, kind, factor, original_len, beta_fast, beta_slow):
+    return lib().fa_rope_freqs(freqs, mscale, rot_dim, theta, kind, factor, original_len,
+                               beta_fast, beta_slow)
+
+
+def fa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count, B, Hkv, T,
+                    d, page, num_pages, max_pages, stream=0):
+    return lib().fa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start,
+                                 count, B, Hkv, T, d, page, num_pages, max_pages, stream)
+
+
+def fa_cache_append_f32(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count, B,
+                        Hkv, T, d, page, num_pages, max_pages, stream=0):
+    return lib().fa_cache_append_f32(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start,
+                                     count, B, Hkv, T, d, page, num_pages, max_pages, stream)
+
+
+def fa_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B, Hkv, N, d, page,
+                  num_pages, max_pages, stream=0):
+    return lib().fa_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B, Hkv,
+                               N, d, page, num_pages, max_pages, stream)
+
+
+def fa_cache_read_f32(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B, Hkv, N, d,
+                      page, num_pages, max_pages, stream=0):
+    return lib().fa_cache_read_f32(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B,
+                                   Hkv, N, d, page, num_pages, max_pages, stream)
+
+
+def fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d):
+    return int(lib().fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d))
+
+
+def fa_fwd_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, ws, B, Hq, Hkv,
+                 Nq, d, page, num_pages, max_pages, scale, causal, stream=0):
+    return lib().fa_fwd_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, ws,
+                              B, Hq, Hkv, Nq, d, page, num_pages, max_pages, scale, int(causal),
+                              stream)
 
 
 def fa_device_status(stream=0):
@@ -382,3 +467,191 @@ def backward(q, k, v, o, lse, dout, scale=None, causal=False, workspace=None):
                   workspace.data_ptr(), B, Hq, Hkv, Nq, Nk, d, scale, causal, _stream(q)),
                fn.__name__)
     return dq, dk, dv
+
+
+# ------------------------------------------------- rotary positions, 8-bit cache
+def rope_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=4096,
+               beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """(freqs, mscale) for ``rope``: the float64 frequency table [rot_dim / 2]
+    on `device` and the factor on the rotated values, scaled for long contexts
+    ("none", "linear", "ntk" or "yarn", fa_rope_freqs)."""
+    import torch
+    if scaling not in FA_ROPE_KINDS:
+        raise ValueError(f"rope_freqs: scaling must be one of {tuple(FA_ROPE_KINDS)}")
+    if rot_dim <= 0:
+        raise ValueError("rope_freqs: rot_dim must be positive")
+    table = (ctypes.c_double * (rot_dim // 2 + 1))()
+    mscale = ctypes.c_float(1.0)
+    _check(fa_rope_freqs(ctypes.addressof(table), ctypes.addressof(mscale), rot_dim, float(theta),
+                         FA_ROPE_KINDS[scaling], float(factor), int(original_len),
+                         float(beta_fast), float(beta_slow)), "fa_rope_freqs")
+    return (torch.tensor(table[:rot_dim // 2], dtype=torch.float64, device=device),
+            float(mscale.value))
+
+
+def _rope(where, q, k, positions, freqs, mscale, interleaved, out, fn_bf16, fn_f32):
+    import torch
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{where}: q must be [B, Hq, N, d], bfloat16 or float32")
+    B, Hq, N, d = q.shape
+    Hkv = 0
+    if k is not None:
+        if (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != N
+                or k.shape[3] != d):
+            raise ValueError(f"{where}: k must be [B, Hkv, N, d] of q's dtype")
+        Hkv = k.shape[1]
+    per_batch = positions.dim() == 2
+    if (positions.dtype != torch.int32
+            or tuple(positions.shape) != ((B, N) if per_batch else (N,))):
+        raise ValueError(f"{where}: positions must be int32 [B, N] or [N]")
+    if freqs.dim() != 1 or freqs.dtype != torch.float64:
+        raise ValueError(f"{where}: freqs must be float64 [rot_dim / 2]")
+    if out is None:
+        qo = torch.empty_like(q)
+        ko = None if k is None else torch.empty_like(k)
+    else:
+        qo, ko = out
+        for name, t, o in (("q", q, qo), ("k", k, ko)):
+            if (o is None) != (t is None) or (t is not None and (o.shape != t.shape
+                                                                 or o.dtype != t.dtype)):
+                raise ValueError(f"{where}: out must be shaped and typed like (q, k)")
+    _check_cuda(where, q, positions, freqs, qo, *(() if k is None else (k, ko)))
+    fn = fn_bf16 if q.dtype == torch.bfloat16 else fn_f32
+    with _on(q):
+        _check(fn(q.data_ptr(), 0 if k is None else k.data_ptr(), qo.data_ptr(),
+                  0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(), B, Hq,
+                  Hkv, N, d, 2 * freqs.shape[0], per_batch, interleaved, float(mscale),
+                  _stream(q)), fn.__name__)
+    return qo, ko
+
+
+def rope(q, k, positions, freqs, mscale=1.0, interleaved=False, out=None):
+    """(q', k'): rotary positions on q [B, Hq, N, d] and k [B, Hkv, N, d] (k
+    may be None), bfloat16 or float32, in one launch (fa_rope, fa_rope_f32).
+    positions: int32 [B, N] or [N]; freqs, mscale: ``rope_freqs``.  out=(q, k)
+    turns in place."""
+    return _rope("rope", q, k, positions, freqs, mscale, interleaved, out, fa_rope, fa_rope_f32)
+
+
+def rope_backward(dq, dk, positions, freqs, mscale=1.0, interleaved=False, out=None):
+    """Gradients of ``rope``'s inputs from those of its outputs (fa_rope_bwd,
+    fa_rope_bwd_f32); dk may be None."""
+    return _rope("rope_backward", dq, dk, positions, freqs, mscale, interleaved, out, fa_rope_bwd,
+                 fa_rope_bwd_f32)
+
+
+def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, d, *arrays):
+    """The cache's tensors against B, Hkv, d; `arrays`: (name, int32 [B] tensor
+    or None) pairs.  Returns (page, num_pages, max_pages)."""
+    import torch
+    f8 = (torch.float8_e4m3fn, torch.uint8)
+    if (k_cache.dim() != 4 or k_cache.dtype not in f8 or k_cache.shape[1] != Hkv
+            or k_cache.shape[3] != d or v_cache.shape != k_cache.shape
+            or v_cache.dtype not in f8):
+        raise ValueError(f"{where}: k_cache and v_cache must be E4M3 [num_pages, Hkv, page, d]")
+    num_pages, _, page, _ = k_cache.shape
+    shape = (num_pages, Hkv)
+    if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype != torch.float32
+            or v_scale.dtype != torch.float32):
+        raise ValueError(f"{where}: k_scale and v_scale must be float32 [num_pages, Hkv]")
+    if (block_table.dim() != 2 or block_table.shape[0] != B
+            or block_table.dtype != torch.int32):
+        raise ValueError(f"{where}: block_table must be int32 [B, max_pages]")
+    present = []
+    for name, t in arrays:
+        if t is None:
+            continue
+        if t.shape != (B,) or t.dtype != torch.int32:
+            raise ValueError(f"{where}: {name} must be int32 [B]")
+        present.append(t)
+    _check_cuda(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, *present)
+    return page, num_pages, block_table.shape[1]
+
+
+def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None):
+    """Write new tokens k, v [B, Hkv, T, d] (bfloat16 or float32) of each
+    sequence at positions start[b] .. into the paged E4M3 cache, with one
+    power-of-two scale per page and head (fa_cache_append).  count: int32 [B]
+    tokens of each sequence that count (None: all T).  The cache tensors are
+    updated in place."""
+    import torch
+    if (k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype
+            or k.dtype not in (torch.bfloat16, torch.float32)):
+        raise ValueError("cache_append: k and v must both be [B, Hkv, T, d], bfloat16 or float32")
+    B, Hkv, T, d = k.shape
+    if start is None:
+        raise ValueError("cache_append: start must be int32 [B]")
+    page, num_pages, max_pages = _check_cache("cache_append", k, k_cache, v_cache, k_scale, v_scale,
+                                              block_table, B, Hkv, d, ("start", start),
+                                              ("count", count))
+    _check_cuda("cache_append", k, v)
+    fn = fa_cache_append if k.dtype == torch.bfloat16 else fa_cache_append_f32
+    with _on(k):
+        _check(fn(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                  k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                  start.data_ptr(), 0 if count is None else count.data_ptr(), B, Hkv, T, d, page,
+                  num_pages, max_pages, _stream(k)), fn.__name__)
+
+
+def cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, N, dtype=None):
+    """Dense k, v [B, Hkv, N, d] (bfloat16, or dtype=torch.float32): the first
+    N tokens of each sequence out of the cache, zeros from lens[b] on
+    (fa_cache_read)."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("cache_read: dtype must be bfloat16 or float32")
+    if k_cache.dim() != 4 or block_table.dim() != 2 or lens is None:
+        raise ValueError("cache_read: k_cache must be [num_pages, Hkv, page, d], block_table "
+                         "int32 [B, max_pages], lens int32 [B]")
+    _, Hkv, _, d = k_cache.shape
+    B = block_table.shape[0]
+    page, num_pages, max_pages = _check_cache("cache_read", k_cache, k_cache, v_cache, k_scale,
+                                              v_scale, block_table, B, Hkv, d, ("lens", lens))
+    k = torch.empty(B, Hkv, N, d, device=k_cache.device, dtype=dtype)
+    v = torch.empty_like(k)
+    fn = fa_cache_read if dtype == torch.bfloat16 else fa_cache_read_f32
+    with _on(k_cache):
+        _check(fn(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  block_table.data_ptr(), lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, N,
+                  d, page, num_pages, max_pages, _stream(k_cache)), fn.__name__)
+    return k, v
+
+
+def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
+                  workspace=None):
+    """O (bfloat16), L of query tokens q [B, Hq, Nq, d] (bfloat16) over the
+    first lens[b] tokens of each sequence of the paged E4M3 cache
+    (fa_fwd_cache).  Causal is bottom-right aligned: the queries are the last
+    Nq of those tokens.  A query that sees no key gets O = 0, L = -inf."""
+    import torch
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or k_cache.dim() != 4:
+        raise ValueError("forward_cache: q must be bfloat16 [B, Hq, Nq, d], k_cache "
+                         "[num_pages, Hkv, page, d]")
+    B, Hq, Nq, d = q.shape
+    Hkv = k_cache.shape[1]
+    if lens is None:
+        raise ValueError("forward_cache: lens must be int32 [B]")
+    page, num_pages, max_pages = _check_cache("forward_cache", q, k_cache, v_cache, k_scale,
+                                              v_scale, block_table, B, Hkv, d, ("lens", lens))
+    scale = d ** -0.5 if scale is None else float(scale)
+    need = fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d)
+    if workspace is None:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+    elif (not workspace.is_cuda or not workspace.is_contiguous()
+          or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"forward_cache: workspace must be a contiguous CUDA buffer of at least "
+                         f"{need} bytes")
+    elif workspace.device != q.device:
+        raise ValueError(f"forward_cache: workspace must be on q's device ({q.device}); "
+                         f"got {workspace.device}")
+    o = torch.empty_like(q)
+    L = torch.empty(B, Hq, Nq, device=q.device, dtype=torch.float32)
+    with _on(q):
+        _check(fa_fwd_cache(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                            lens.data_ptr(), o.data_ptr(), L.data_ptr(),
+                            0 if workspace is None else workspace.data_ptr(), B, Hq, Hkv, Nq, d,
+                            page, num_pages, max_pages, scale, causal, _stream(q)),
+               "fa_fwd_cache")
+    return o, L

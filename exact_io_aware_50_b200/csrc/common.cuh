@@ -23,6 +23,7 @@ constexpr long long kWaitLimitNs = 1000000000LL;
 enum ErrorBits : unsigned {
   kErrTimeout = 1u,   // a bounded wait expired
   kErrConfig = 2u,    // a kernel refused to run (e.g. misaligned shared memory)
+  kErrPage = 4u,      // a cache kernel met a page number, position or length out of range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

@@ -139,6 +139,7 @@ FA_EXPORT const char *fa_strerror(int status) {
     case FA_ERR_ARCH: return "device is not compute capability 10.0 (sm_100a build)";
     case FA_ERR_CUDA: return "CUDA runtime error or kernel launch failure";
     case FA_ERR_TIMEOUT: return "a bounded in-kernel wait expired";
+    case FA_ERR_PAGE: return "a cache call met a page number, position or length out of range";
     default: return "unknown status";
   }
 }
@@ -434,7 +435,8 @@ FA_EXPORT int fa_device_status(fa_stream_t stream) {
   if (host && cudaMemcpy(err, &zero, sizeof(unsigned), cudaMemcpyHostToDevice) != cudaSuccess)
     return FA_ERR_CUDA;
   if (host & fa::kErrTimeout) return FA_ERR_TIMEOUT;
-  return host ? FA_ERR_CUDA : FA_OK;
+  if (host & fa::kErrConfig) return FA_ERR_CUDA;
+  return host & fa::kErrPage ? FA_ERR_PAGE : FA_OK;
 }
 
 FA_EXPORT int fa_wait_selftest(long long timeout_ns, fa_stream_t stream) {

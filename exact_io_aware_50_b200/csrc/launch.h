@@ -77,6 +77,41 @@ int launch_bwd_dkdv_bf16_sm100(const AttnArgs &a);
 int launch_bwd_dq_bf16(const AttnArgs &a);       // dq = bf16(scale * accumulator)
 int launch_wait_selftest(long long timeout_ns, cudaStream_t stream, unsigned *err);
 
+// Rotary positions (fa_rope.cu).
+struct RopeArgs {
+  const void *q = nullptr, *k = nullptr;
+  void *q_out = nullptr, *k_out = nullptr;
+  const int *positions = nullptr;
+  const double *freqs = nullptr;
+  int B = 0, Hq = 0, Hkv = 0, N = 0, d = 0, rot = 0;
+  int pos_per_batch = 0, interleaved = 0, backward = 0, f32 = 0;
+  float mscale = 1.f;
+  cudaStream_t stream = nullptr;
+};
+int launch_rope(const RopeArgs &a);
+
+// The paged E4M3 cache (fa_cache.cu) and attention over it (fa_fwd_cache.cu).
+struct CacheArgs {
+  const void *k = nullptr, *v = nullptr;     // append: new tokens [B, Hkv, T, d]
+  void *k_out = nullptr, *v_out = nullptr;   // read: dense tokens [B, Hkv, T, d]
+  uint8_t *k_cache = nullptr, *v_cache = nullptr;
+  float *k_scale = nullptr, *v_scale = nullptr;
+  const int *table = nullptr, *start = nullptr, *count = nullptr, *lens = nullptr;
+  const void *q = nullptr;                   // attention
+  void *o = nullptr, *ws = nullptr;
+  float *lse = nullptr;
+  int B = 0, Hq = 0, Hkv = 0, Nq = 0, T = 0, d = 0;
+  int page = 0, num_pages = 0, max_pages = 0;
+  int causal = 0, f32 = 0;
+  float scale = 0.f;
+  cudaStream_t stream = nullptr;
+  unsigned *err = nullptr;
+};
+int launch_cache_append(const CacheArgs &a);
+int launch_cache_read(const CacheArgs &a);
+int launch_fwd_cache(const CacheArgs &a);
+size_t fwd_cache_ws_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
 // Argument checks and per-call device set-up shared by the C entry points
 // (fa_status codes): size/scale rules, then current device, architecture and
 // the device error word.

@@ -55,7 +55,9 @@ typedef enum {
   FA_ERR_ALIGNMENT = 3,   /* a pointer is not 16-byte aligned */
   FA_ERR_ARCH = 4,        /* current device is not compute capability 10.0 */
   FA_ERR_CUDA = 5,        /* a CUDA runtime call or kernel launch failed */
-  FA_ERR_TIMEOUT = 6      /* a bounded in-kernel wait expired (reported by fa_device_status) */
+  FA_ERR_TIMEOUT = 6,     /* a bounded in-kernel wait expired (reported by fa_device_status) */
+  FA_ERR_PAGE = 7         /* a cache call met a page number or length outside its cache or table
+                             (reported by fa_device_status) */
 } fa_status;
 
 /*
@@ -274,12 +276,156 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o,
                    fa_stream_t stream);
 
 /*
+ * Rotary positions.  Pair p (0 <= p < rot_dim / 2) of a row at position t
+ * turns by the angle a = t * freqs[p]:
+ *     (x, y) -> mscale * (x cos a - y sin a, y cos a + x sin a).
+ * interleaved == 0: x is column p, y column p + rot_dim / 2 (halves);
+ * interleaved != 0: x is column 2p, y column 2p + 1.  Columns rot_dim and up
+ * are copied.  The angle is formed and reduced in float64 (positions of
+ * millions keep their angle), the rotation runs in float32 and is rounded
+ * once to the tensors' type.
+ *
+ * q, q_out [B, Hq, N, d]; k, k_out [B, Hkv, N, d]: bfloat16 (fa_rope,
+ * fa_rope_bwd) or float32 (the _f32 forms); one launch turns both.  k and
+ * k_out may both be NULL (Hkv is then ignored).  An output may be its input
+ * (in place); it must not overlap it otherwise.
+ * positions: int32 in device memory, [B, N] (pos_per_batch != 0) or [N]
+ * shared by the batch; any value, negative ones included.
+ * freqs: float64 [rot_dim / 2] in device memory (fa_rope_freqs fills such a
+ * table on the host).  mscale: finite and > 0, else FA_ERR_INVALID_ARG.
+ * d: a multiple of 4, at most 256; rot_dim: a multiple of 8, at most d
+ * (FA_ERR_UNSUPPORTED otherwise).
+ *
+ * fa_rope_bwd(dq_out, dk_out, dq, dk): the gradient, i.e. the transposed map
+ *     (x, y) -> mscale * (x cos a + y sin a, y cos a - x sin a),
+ * with columns rot_dim and up copied.  Same arguments and rules.
+ */
+int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions,
+            const double *freqs, int B, int Hq, int Hkv, int N, int d, int rot_dim,
+            int pos_per_batch, int interleaved, float mscale, fa_stream_t stream);
+int fa_rope_f32(const float *q, const float *k, float *q_out, float *k_out, const int *positions,
+                const double *freqs, int B, int Hq, int Hkv, int N, int d, int rot_dim,
+                int pos_per_batch, int interleaved, float mscale, fa_stream_t stream);
+int fa_rope_bwd(const void *dq_out, const void *dk_out, void *dq, void *dk, const int *positions,
+                const double *freqs, int B, int Hq, int Hkv, int N, int d, int rot_dim,
+                int pos_per_batch, int interleaved, float mscale, fa_stream_t stream);
+int fa_rope_bwd_f32(const float *dq_out, const float *dk_out, float *dq, float *dk,
+                    const int *positions, const double *freqs, int B, int Hq, int Hkv, int N,
+                    int d, int rot_dim, int pos_per_batch, int interleaved, float mscale,
+                    fa_stream_t stream);
+
+/*
+ * fa_rope_freqs -- fills the HOST array freqs[rot_dim / 2] (float64) and, when
+ * mscale is not NULL, *mscale, with f_p = theta^(-2p / rot_dim) scaled for a
+ * context `factor` times the trained one:
+ *   FA_ROPE_PLAIN   f_p (factor ignored)
+ *   FA_ROPE_LINEAR  f_p / factor
+ *   FA_ROPE_NTK     theta replaced by theta * factor^(rot_dim / (rot_dim - 2))
+ *   FA_ROPE_YARN    (1 - g) f_p / factor + g f_p with
+ *                   g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1),
+ *                   r = original_len * f_p / (2 pi) the turns within the
+ *                   trained length (Peng et al., "YaRN: Efficient Context
+ *                   Window Extension of Large Language Models", section 3);
+ *                   *mscale = 0.1 ln(factor) + 1
+ * *mscale is 1 for the other kinds.  Touches no device.  FA_ERR_INVALID_ARG
+ * for a null freqs, rot_dim <= 0, theta <= 0, an unknown kind, and (other
+ * than FA_ROPE_PLAIN) factor < 1, or original_len <= 0 or beta_fast <=
+ * beta_slow for FA_ROPE_YARN, or values that are not finite;
+ * FA_ERR_UNSUPPORTED when rot_dim is no multiple of 8 or above 256.
+ */
+enum { FA_ROPE_PLAIN = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_YARN = 3 };
+int fa_rope_freqs(double *freqs, float *mscale, int rot_dim, double theta, int kind, double factor,
+                  int original_len, double beta_fast, double beta_slow);
+
+/*
+ * The 8-bit key/value cache.  Keys and values of a batch of sequences live in
+ * pages of `page` tokens (16, 32, 64 or 128):
+ *     k_cache, v_cache : [num_pages, Hkv, page, d]  OCP E4M3 codes
+ *     k_scale, v_scale : [num_pages, Hkv]           float32
+ *     block_table      : [B, max_pages]             int32
+ * Token j of sequence b stands in slot j % page of page
+ * block_table[b][j / page]; the value meant is scale * code value.  A page is
+ * the block of tokens that shares one scale per head.  d = 64, 128 or 256.
+ * Every array is in device memory, dense, and owned by the caller; tensors of
+ * tokens and caches are 16-byte aligned, the int32 and float32 arrays 4-byte.
+ *
+ * Page numbers are checked by the kernels: a token whose page number is
+ * outside [0, num_pages), or whose place is outside the table's max_pages
+ * pages, is left out (not written; read as zeros; hidden from every query),
+ * a negative length counts as 0, and fa_device_status reports FA_ERR_PAGE.
+ *
+ * fa_cache_append -- writes T new tokens of each sequence at positions
+ * start[b] .. start[b] + n_b - 1, n_b = count ? min(count[b], T) : T (tokens
+ * n_b and up of a padded batch are not written).  k, v: [B, Hkv, T, d]
+ * bfloat16 (fa_cache_append) or float32 (fa_cache_append_f32); start, count:
+ * int32 [B]; count may be NULL.
+ * For each touched (page, head) and each of K and V, with amax the largest
+ * finite magnitude among the new values of that page,
+ *     need  = the least power of two s >= 2^-112 with amax <= 448 s,
+ *     scale = need                when the call writes the page's slot 0,
+ *             max(scale, need)    otherwise (the page holds older tokens),
+ * and the older slots' codes become E4M3(code * old scale / new scale) when
+ * the scale grows: by a power of two, so only codes that fall below 2^-6 are
+ * rounded again.  New codes are E4M3(x / scale), round to nearest even;
+ * infinities become +-448, NaN stays NaN.  Slots behind the last new token
+ * keep their bytes.
+ * No page may be written for two sequences, or twice, in one call (the result
+ * is then undefined).
+ *
+ * fa_cache_read -- the first N tokens of each sequence back as dense k, v
+ * [B, Hkv, N, d], bfloat16 (fa_cache_read: scale * code rounded to nearest
+ * even; exact for scales that are powers of two) or float32
+ * (fa_cache_read_f32).  Rows lens[b] and up are zero.  lens: int32 [B].
+ */
+int fa_cache_append(const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale,
+                    float *v_scale, const int *block_table, const int *start, const int *count,
+                    int B, int Hkv, int T, int d, int page, int num_pages, int max_pages,
+                    fa_stream_t stream);
+int fa_cache_append_f32(const float *k, const float *v, void *k_cache, void *v_cache,
+                        float *k_scale, float *v_scale, const int *block_table, const int *start,
+                        const int *count, int B, int Hkv, int T, int d, int page, int num_pages,
+                        int max_pages, fa_stream_t stream);
+int fa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale,
+                  const float *v_scale, const int *block_table, const int *lens, void *k, void *v,
+                  int B, int Hkv, int N, int d, int page, int num_pages, int max_pages,
+                  fa_stream_t stream);
+int fa_cache_read_f32(const void *k_cache, const void *v_cache, const float *k_scale,
+                      const float *v_scale, const int *block_table, const int *lens, float *k,
+                      float *v, int B, int Hkv, int N, int d, int page, int num_pages,
+                      int max_pages, fa_stream_t stream);
+
+/*
+ * fa_fwd_cache -- attention of Nq query tokens per sequence over the cache:
+ *     O = softmax(scale * Q K^T [+ causal]) V,   L = log-sum-exp (natural),
+ * with K, V the first lens[b] tokens of sequence b.  q, o: bfloat16
+ * [B, Hq, Nq, d]; lse: float32 [B, Hq, Nq]; query head h reads key/value head
+ * h / (Hq / Hkv).  causal != 0: the queries are the last Nq tokens of their
+ * sequence (append them first), so query i sees keys j <= lens[b] - Nq + i,
+ * the split-KV forward's bottom-right mask with a length of its own for each
+ * sequence; causal == 0: every key.  A query that sees no key gets O = 0,
+ * L = -inf.  Slots behind a sequence's length may hold anything.
+ * Scores, the softmax statistics and O are float32; the codes enter the
+ * matrix instructions exactly, the weights exp(s - m) rounded once to 11 bits.
+ * k_scale, v_scale: finite and > 0, as fa_cache_append writes them.
+ *
+ * workspace: fa_fwd_cache_workspace_size(...) bytes, 256-byte aligned
+ * (NULL when that is 0); contents ignored on entry and clobbered, so calls
+ * that may overlap on the GPU (two graphs, two streams) need one each.
+ */
+size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+int fa_fwd_cache(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                 const float *v_scale, const int *block_table, const int *lens, void *o, float *lse,
+                 void *workspace, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages,
+                 int max_pages, float scale, int causal, fa_stream_t stream);
+
+/*
  * fa_device_status -- synchronises `stream`, then reads and clears the
  * library's device error word on the current device.  Returns FA_OK, or
  * FA_ERR_TIMEOUT when a kernel's bounded wait expired since the last call
  * (that kernel then returned early and its outputs are undefined), or
  * FA_ERR_CUDA when the synchronisation itself failed or a kernel refused to
- * run (its shared memory was not 1024-byte aligned).
+ * run (its shared memory was not 1024-byte aligned), or FA_ERR_PAGE when a
+ * cache call left tokens out (bad page number, position or length).
  */
 int fa_device_status(fa_stream_t stream);
 
