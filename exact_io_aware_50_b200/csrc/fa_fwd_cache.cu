@@ -1,9 +1,31 @@
 // fa_fwd_cache.cu -- attention over the paged E4M3 cache.
 //
-//     s_j = scale * sk * (q . K^_j),  m = max s,  l = sum e^{s_j - m},
-//     O = sum e^{s_j - m} sv V^_j / l,  L = m + ln l
+//     s_j = scale * sk * (q . K^_j),  m = max s,  l = sum 2^{s_j - m},
+//     O = sum 2^{s_j - m} sv V^_j / l,  L = (m + log2 l) ln 2
 //
-// with sk, sv the scales of the page that token j stands in.
+// with s in base-2 units, sk and sv the scales of the page token j stands in.
+//
+// Rows: the g * Nq query rows that read one key/value head (contiguous in q)
+// are cut into tiles of 16 * MT rows, so a page is read once for all of them.
+// Work: a unit is (sequence, key/value head, row tile); its tokens come in
+// granules of 64.  The granules of all units, in one line, are divided evenly
+// among the CTAs (two per SM), so ragged lengths, few heads and long caches
+// all fill the GPU: a CTA's run may start inside one unit and end inside
+// another.  A unit that one CTA covers is finished there; the others leave
+// their normalised partial O and log-sum-exp in the workspace, and the merge
+// kernel joins them (L = log sum 2^{L_c}, O = sum 2^{L_c - L} O_c).  Nothing
+// is accumulated by atomics: results do not depend on timing.
+//
+// A warp takes 16 tokens of each granule.  It keeps its own ring of shared
+// memory, filled by 16-byte asynchronous copies, and its own (m, l, O): the
+// four warps meet only at the end of a unit.  The E4M3 codes become halves,
+// exactly, on their way into mma.m16n8k16; q becomes halves too, each row
+// times a power of two that brings its largest entry to [2^13, 2^14), so an
+// entry keeps its 8 bits unless it is 2^-28 of the largest.  The weight that
+// multiplies V is 2^{s - m} sv, rounded to a half.  It has a reference M of its
+// own, the running maximum of s + log2 sv: terms down to 2^-26 of the largest
+// keep 11 bits whatever the pages' scales, and smaller ones err by at most
+// 2^-37 of the largest weight.
 #include <math.h>
 
 #include "cache.cuh"
@@ -11,73 +33,636 @@
 namespace fa {
 namespace {
 
-// One CTA per query row; each warp takes every fourth token, a lane D / 32
-// columns; the four warps' (m, l, O) are merged at the end.
+constexpr int kWarps = 4;
+constexpr int kStep = 16;                       // tokens a warp takes at a time
+constexpr int kGranule = kWarps * kStep;
+constexpr int kRingBytes = 24 * 1024;           // per warp
+constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
+constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
+
+template <int D, int MT>
+struct RowCfg {
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int CH = D / 16;             // 16-byte chunks of a token
+  static constexpr int STAGE = 2 * kStep * D;   // K then V codes of a step
+  static constexpr int STAGES = kRingBytes / STAGE;
+  static constexpr int OFF_META = kWarps * kRingBytes;
+  static constexpr int OFF_STAT = OFF_META + kWarps * STAGES * 16;
+  static constexpr int SMEM = OFF_STAT + kWarps * ROWS * 4;
+  static_assert(ROWS * D * 4 <= kRingBytes, "a warp's O fits in its ring");
+  static_assert(STAGES >= 3, "ring depth");
+};
+
+// Byte offset of 16-byte chunk c of token r in a step's tile: chunks are
+// permuted so that eight tokens' chunk c lie in eight different bank groups.
 template <int D>
-__global__ void fwd_cache_row_kernel(const CacheArgs a) {
-  constexpr int PER = D / 32;
-  __shared__ float s_m[4], s_l[4], s_o[4][D];
-  const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z;
-  const int h = hq / (a.Hq / a.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = checked_len(a.lens, b, a.max_pages, a.page, a.err);
-  const int lim = a.causal ? min(len, len - a.Nq + i + 1) : len;
-  const long long row = ((long long)b * a.Hq + hq) * a.Nq + i;
-  float q[PER], acc[PER];
-  for (int e = 0; e < PER; ++e) {
-    q[e] = __bfloat162float(((const __nv_bfloat16 *)a.q)[row * D + lane * PER + e]) * a.scale;
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < lim; j += 4) {
-    const int pg = checked_page(a.table, (long long)b * a.max_pages + j / a.page, a.num_pages, a.err);
-    if (pg < 0) continue;
-    const long long page_h = (long long)pg * a.Hkv + h;
-    const long long at = (page_h * a.page + j % a.page) * D + lane * PER;
-    float s = 0.f;
-    for (int e = 0; e < PER; ++e) s += q[e] * e4m3x2_to_float2(a.k_cache[at + e]).x;
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.k_scale[page_h];
-    const float m_new = fmaxf(m, s);
-    const float alpha = m == -INFINITY ? 0.f : __expf(m - m_new), p = expf(s - m_new);
-    m = m_new;
-    l = l * alpha + p;
-    const float pv = p * a.v_scale[page_h];
-    for (int e = 0; e < PER; ++e)
-      acc[e] = acc[e] * alpha + pv * e4m3x2_to_float2(a.v_cache[at + e]).x;
-  }
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-  for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return r * D + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// c += A B: 16 x 16 halves, 16 x 8 halves, float32 accumulator.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
+struct RowParams {
+  const __nv_bfloat16 *q;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int *table, *lens;
+  __nv_bfloat16 *o;
+  float *lse;
+  float *o_part, *l_part;   // [grid][2][ROWS][D], [grid][2][ROWS] (base 2)
+  int B, Hq, Hkv, Nq, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
+  int page_log2, num_pages, max_pages;
+  int causal, ctas;
+  float scale_log2;
+  unsigned *err;
+};
+
+__device__ __forceinline__ int granules_of(const RowParams &p, int b) {
+  const int n = p.lens[b];
+  return (min(max(n, 0), p.max_pages << p.page_log2) + kGranule - 1) / kGranule;
+}
+
+// Sum over the block of a value per thread (every thread gets it).
+__device__ __forceinline__ long long block_sum(long long v, long long *s_red) {
+  const int nw = blockDim.x >> 5;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   __syncthreads();
-  const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float w[4], tot = 0.f;
-  for (int u = 0; u < 4; ++u) {
-    w[u] = s_m[u] == -INFINITY ? 0.f : expf(s_m[u] - mm);
-    tot += w[u] * s_l[u];
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  long long t = 0;
+  for (int w = 0; w < nw; ++w) t += s_red[w];
+  return t;
+}
+
+// The line of granules: sequences in order, each with Hkv * tiles units of
+// granules_of(b).  Gives the total and the granules before sequence b.
+__device__ __forceinline__ void line_of(const RowParams &p, int b, long long *s_red, long long *total,
+                                        long long *before) {
+  long long all = 0, pre = 0;
+  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+    const int n = granules_of(p, i);
+    all += n;
+    if (i < b) pre += n;
   }
-  const float inv = tot > 0.f || tot != tot ? 1.f / tot : 0.f;
-  for (int c = threadIdx.x; c < D; c += blockDim.x) {
-    float o = 0.f;
-    for (int u = 0; u < 4; ++u) o += w[u] * s_o[u][c];
-    ((__nv_bfloat16 *)a.o)[row * D + c] = __float2bfloat16(o * inv);
+  const long long units = (long long)p.Hkv * p.tiles;
+  *total = block_sum(all, s_red) * units;
+  *before = b > 0 ? block_sum(pre, s_red) * units : 0;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const RowParams p) {
+  using C = RowCfg<D, MT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_red[kWarps];
+  __shared__ int s_b;
+  __shared__ long long s_before;
+  const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int units = p.Hkv * p.tiles;
+
+  // This CTA's run of the line, and the sequence it starts in.
+  long long total, unused;
+  line_of(p, 0, s_red, &total, &unused);
+  const long long per = (total + p.ctas - 1) / p.ctas;
+  long long pos = per * blockIdx.x;
+  const long long end = min(total, pos + per);
+  if (pos >= end) return;
+  {
+    long long base = 0;   // granules of the sequences before this chunk of 128
+    for (int i0 = 0; i0 < p.B; i0 += blockDim.x) {
+      const int i = i0 + (int)threadIdx.x;
+      const long long n = i < p.B ? (long long)granules_of(p, i) * units : 0;
+      long long inc = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      __syncthreads();
+      if (lane == 31) s_red[warp] = inc;
+      __syncthreads();
+      long long pre = base, chunk = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) pre += s_red[w];
+        chunk += s_red[w];
+      }
+      inc += pre;
+      if (pos >= inc - n && pos < inc) {
+        s_b = i;
+        s_before = inc - n;
+      }
+      base += chunk;
+      if (base > pos) break;   // uniform: found in this chunk
+    }
+    __syncthreads();
   }
-  if (threadIdx.x == 0) a.lse[row] = tot == 0.f ? -INFINITY : mm + logf(tot);
+  int b = s_b;
+  long long b_first = s_before;
+
+  const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+  float4 *meta = reinterpret_cast<float4 *>(smem + C::OFF_META) + warp * C::STAGES;
+  float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);   // [warp][ROWS]
+
+  while (pos < end) {
+    int ng = granules_of(p, b);
+    while (pos >= b_first + (long long)ng * units) {   // next sequence with tokens
+      b_first += (long long)ng * units;
+      ++b;
+      ng = granules_of(p, b);
+    }
+    const int u = (int)((pos - b_first) / ng);
+    const int g0 = (int)(pos - b_first - (long long)u * ng);
+    const int g1 = (int)min((long long)ng, g0 + (end - pos));
+    pos += g1 - g0;
+    const int h = u / p.tiles, r0 = (u - h * p.tiles) * C::ROWS;
+    if (threadIdx.x == 0) (void)checked_len(p.lens, b, p.max_pages, 1 << p.page_log2, p.err);
+    const int len = min(max(p.lens[b], 0), p.max_pages << p.page_log2);
+    const int group = p.Hq / p.Hkv;
+    const long long row_base = ((long long)b * p.Hq + (long long)h * group) * p.Nq;   // row 0 of q, o, lse
+
+    // ---- q: A fragments of halves, each row times a power of two
+    uint32_t qa[MT][C::CH][4];
+    float row_c[MT][2];        // scale * log2 e / that power of two
+    int lim[MT][2];            // keys [0, lim) visible
+    int lim_min = len;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + mt * 16 + g + 8 * e;
+        const bool live = r < p.R;
+        const __nv_bfloat16 *src = p.q + (row_base + (live ? r : 0)) * D + 4 * t;
+        uint2 raw[C::CH];
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) {
+          raw[c] = live ? *reinterpret_cast<const uint2 *>(src + 16 * c) : make_uint2(0u, 0u);
+          const uint32_t w[2] = {raw[c].x, raw[c].y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] << 16)));
+            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // mx in [2^k, 2^{k+1}); zero rows and exponents past float32's reach are cut off
+        const int k = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
+        const float up = __uint_as_float((uint32_t)(13 - k + 127) << 23);
+        row_c[mt][e] = p.scale_log2 * __uint_as_float((uint32_t)(k - 13 + 127) << 23);
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) {
+          qa[mt][c][e] = pack_half2(__uint_as_float(raw[c].x << 16) * up,
+                                    __uint_as_float(raw[c].x & 0xFFFF0000u) * up);
+          qa[mt][c][2 + e] = pack_half2(__uint_as_float(raw[c].y << 16) * up,
+                                        __uint_as_float(raw[c].y & 0xFFFF0000u) * up);
+        }
+        lim[mt][e] = !live ? 0 : (p.causal ? max(0, len - p.Nq + r % p.Nq + 1) : len);
+        if (live) lim_min = min(lim_min, lim[mt][e]);
+      }
+    }
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+
+    float o[MT][D / 8][4];
+    float m_s[MT][2], m_o[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_s[mt][e] = m_o[mt][e] = -INFINITY;
+        l[mt][e] = 0.f;
+      }
+    }
+
+    // ---- pages: lane i holds page, sk and log2 sv of step 32 k + i
+    const int steps = g1 - g0;
+    const int *tab = p.table + (long long)b * p.max_pages;
+    auto token_of = [&](int s) { return ((g0 + s) * kWarps + warp) * kStep; };
+    struct Pages {
+      int pg;
+      float sk, lsv;
+    };
+    auto lookup = [&](int s) {
+      Pages x{-1, 0.f, 0.f};
+      const int j = token_of(s);
+      if (s < steps && j < len) {
+        x.pg = checked_page(tab, j >> p.page_log2, p.num_pages, p.err);
+        if (x.pg >= 0) {
+          x.sk = p.k_scale[(long long)x.pg * p.Hkv + h];
+          x.lsv = log2f(p.v_scale[(long long)x.pg * p.Hkv + h]);
+        }
+      }
+      return x;
+    };
+    Pages cur = lookup(lane), nxt = lookup(32 + lane);
+    // Copies of step s into its stage; always one commit group a step.
+    auto issue = [&](int s) {
+      if (s < steps) {
+        if (s && (s & 31) == 0) {
+          cur = nxt;
+          nxt = lookup(s + 32 + lane);
+        }
+        const int pg = __shfl_sync(0xffffffffu, cur.pg, s & 31);
+        const float sk = __shfl_sync(0xffffffffu, cur.sk, s & 31);
+        const float lsv = __shfl_sync(0xffffffffu, cur.lsv, s & 31);
+        const int j = token_of(s);
+        const int nv = pg < 0 ? 0 : min(kStep, len - j);
+        const int st = s % C::STAGES;
+        if (lane == 0) meta[st] = make_float4(sk, lsv, __int_as_float(nv), 0.f);
+        if (nv > 0) {
+          const long long at = (((long long)pg * p.Hkv + h) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
+          const uint8_t *ks = p.k_cache + at * D, *vs = p.v_cache + at * D;
+          const uint32_t dst = ring + st * C::STAGE;
+          constexpr int RPI = 32 / C::CH;   // tokens a warp-wide copy covers
+#pragma unroll
+          for (int i = 0; i < kStep / RPI; ++i) {
+            const int r = i * RPI + lane / C::CH, c = lane % C::CH;
+            const int src = r < nv ? r * D + c * 16 : 0;   // tokens behind the length: zeros
+            cp_async16(dst + tile_at<D>(r, c), ks + src, r < nv);
+            cp_async16(dst + kStep * D + tile_at<D>(r, c), vs + src, r < nv);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    for (int s = 0; s < C::STAGES - 1; ++s) issue(s);
+
+    for (int s = 0; s < steps; ++s) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();
+      issue(s + C::STAGES - 1);
+      const int st = s % C::STAGES;
+      const float4 mt4 = meta[st];
+      const int nv = __float_as_int(mt4.z);
+      if (nv <= 0) continue;
+      const float sk = mt4.x, lsv = mt4.y;
+      const int j0 = token_of(s);
+      const uint32_t kt = ring + st * C::STAGE, vt = kt + kStep * D;
+
+      // ---- S = q K^T: two groups of 8 tokens
+      float sc[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C::CH; c += 4)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint32_t kb[4];
+          ldsm4(kt + tile_at<D>(8 * n + (lane & 7), c + (lane >> 3)), kb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b0 = e4m3x2_to_half2(kb[i]), b1 = e4m3x2_to_half2(kb[i] >> 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][n], qa[mt][c + i], b0, b1);
+          }
+        }
+
+      // ---- softmax
+      const bool whole = nv == kStep && j0 + kStep <= lim_min;
+      bool moved = false;
+      float mx[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float cf = row_c[mt][e] * sk;
+          const int lm = min(nv, lim[mt][e] - j0);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = sc[mt][n][2 * e + i] * cf;
+              if (!whole && 8 * n + 2 * t + i >= lm) x = -INFINITY;
+              sc[mt][n][2 * e + i] = x;
+            }
+          mx[mt][e] = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]),
+                            fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
+          moved |= mx[mt][e] > fminf(m_s[mt][e], m_o[mt][e] - lsv) + kLag;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = mx[mt][e];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            const float ns = fmaxf(m_s[mt][e], v), no = fmaxf(m_o[mt][e], v + lsv);
+            // a row that has seen no key yet has l = 0 and O = 0
+            const float al = ns == m_s[mt][e] ? 1.f : fast_exp2(m_s[mt][e] - ns);
+            const float ao = no == m_o[mt][e] ? 1.f : fast_exp2(m_o[mt][e] - no);
+            m_s[mt][e] = ns;
+            m_o[mt][e] = no;
+            l[mt][e] *= al;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[mt][n][2 * e] *= ao;
+              o[mt][n][2 * e + 1] *= ao;
+            }
+          }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool none = m_s[mt][e] == -INFINITY;
+          const float ms = none ? 0.f : m_s[mt][e];
+          const float gain = none ? 0.f : fast_exp2(m_s[mt][e] - m_o[mt][e] + lsv + kShift);
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = fast_exp2(sc[mt][n][2 * e] - ms), p1 = fast_exp2(sc[mt][n][2 * e + 1] - ms);
+            sum += p0 + p1;
+            pa[mt][2 * n + e] = pack_half2(p0 * gain, p1 * gain);
+          }
+          l[mt][e] += sum;
+        }
+
+      // ---- a token that some row does not see may hold a NaN code in V, and
+      // 0 * NaN is NaN: such codes become 0, and the columns of the rows that
+      // do see the token become NaN
+      if (j0 + nv > lim_min) {
+#pragma unroll 1
+        for (int w = lane; w < kStep * D / 4; w += 32) {
+          const int r = w / (D / 4), col = (w - r * (D / 4)) * 4;
+          uint32_t *word = reinterpret_cast<uint32_t *>(
+              smem + warp * kRingBytes + st * C::STAGE + kStep * D + tile_at<D>(r, col >> 4) + (col & 15));
+          const uint32_t nan4 = __vcmpeq4(*word & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          unsigned who = __ballot_sync(0xffffffffu, nan4 != 0);
+          if (nan4) *word &= ~nan4;
+          for (; who; who &= who - 1) {
+            const int from = __ffs(who) - 1;
+            const uint32_t bytes = __shfl_sync(0xffffffffu, nan4, from);
+            const int rr = __shfl_sync(0xffffffffu, r, from), cc = __shfl_sync(0xffffffffu, col, from);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int at = 16 * (n >> 1) + (n & 1) + 4 * t + 2 * (e & 1) - cc;   // column within the word
+                  if (at >= 0 && at < 4 && ((bytes >> (8 * at)) & 1u) && j0 + rr < lim[mt][e >> 1])
+                    o[mt][n][e] = __uint_as_float(0x7FC00000u);
+                }
+          }
+        }
+        __syncwarp();
+      }
+
+      // ---- O += P V: ldmatrix.trans hands out pairs of columns of two
+      // tokens; a byte swap makes them pairs of tokens of one column
+#pragma unroll
+      for (int c = 0; c < C::CH; c += 2) {
+        uint32_t vb[4];   // chunk c: tokens 0-7, 8-15; chunk c + 1: the same
+        ldsm4_trans(vt + tile_at<D>((lane & 7) + (lane & 8), c + (lane >> 4)), vb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w0 = __byte_perm(vb[2 * i], 0, 0x3120), w1 = __byte_perm(vb[2 * i + 1], 0, 0x3120);
+          const uint32_t e0 = e4m3x2_to_half2(w0), e1 = e4m3x2_to_half2(w1);
+          const uint32_t d0 = e4m3x2_to_half2(w0 >> 16), d1 = e4m3x2_to_half2(w1 >> 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_f16(o[mt][2 * (c + i)], pa[mt], e0, e1);       // columns 16 (c + i) + 2 n
+            mma_f16(o[mt][2 * (c + i) + 1], pa[mt], d0, d1);   // and + 1
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+
+    // ---- the four warps' results joined: each row's log-sum-exp first
+    float fac[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[mt][e];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        l[mt][e] = v;
+        if (t == 0) stat[warp * C::ROWS + mt * 16 + g + 8 * e] = v == 0.f ? -INFINITY : m_s[mt][e] + log2f(v);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = mt * 16 + g + 8 * e;
+        float top = -INFINITY, sum = 0.f;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
+        for (int w = 0; w < kWarps; ++w)
+          sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : exp2f(stat[w * C::ROWS + r] - top);
+        // O / l_warp * 2^{L_warp - L} = O 2^{M - shift - m} / l * ...
+        fac[mt][e] = l[mt][e] == 0.f ? 0.f
+                                     : exp2f(m_o[mt][e] - kShift - m_s[mt][e]) / l[mt][e] *
+                                           (exp2f(stat[warp * C::ROWS + r] - top) / sum);
+      }
+    // o of columns 16 c + 4 t .. + 3 lies in two accumulators
+    float *mine = reinterpret_cast<float *>(smem + warp * kRingBytes);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) {
+          const float f = fac[mt][e];
+          *reinterpret_cast<float4 *>(mine + (mt * 16 + g + 8 * e) * D + 16 * c + 4 * t) =
+              make_float4(o[mt][2 * c][2 * e] * f, o[mt][2 * c + 1][2 * e] * f,
+                          o[mt][2 * c][2 * e + 1] * f, o[mt][2 * c + 1][2 * e + 1] * f);
+        }
+    __syncthreads();
+    const bool final = g0 == 0 && g1 == ng;
+    const long long part = ((long long)blockIdx.x * 2 + (g0 == 0 ? 1 : 0)) * C::ROWS;
+    const int rows = min(C::ROWS, p.R - r0);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
+      const int r = i / (D / 4), c4 = i - r * (D / 4);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4 *>(smem + w * kRingBytes + (r * D + 4 * c4) * 4);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      }
+      if (final)
+        *reinterpret_cast<uint2 *>(p.o + (row_base + r0 + r) * D + 4 * c4) =
+            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      else
+        *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + 4 * c4) = a;
+    }
+    if ((int)threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      float top = -INFINITY, sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
+      for (int w = 0; w < kWarps; ++w)
+        sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : exp2f(stat[w * C::ROWS + r] - top);
+      const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+      if (final) p.lse[row_base + r0 + r] = L2 * 0.69314718055994531f;
+      else p.l_part[part + r] = L2;
+    }
+    __syncthreads();   // rings and statistics are free again
+  }
+}
+
+// Joins the pieces of the units that several CTAs covered, one CTA per query
+// row; rows of sequences without tokens become O = 0, L = -inf.
+template <int D, int MT>
+__global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p) {
+  using C = RowCfg<D, MT>;
+  __shared__ long long s_red[4];
+  __shared__ float s_o[4][D];
+  const long long row = blockIdx.x;
+  const int b = (int)(row / ((long long)p.Hq * p.Nq));
+  const int hr = (int)(row - (long long)b * p.Hq * p.Nq);   // row within the sequence
+  const int h = hr / p.R, r = hr - h * p.R, tile = r / C::ROWS;
+  const int ng = granules_of(p, b);
+  __nv_bfloat16 *dst = p.o + row * D;
+  if (ng == 0) {
+    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) {
+      p.lse[row] = -INFINITY;
+      if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
+    }
+    return;
+  }
+  long long total, before;
+  line_of(p, b, s_red, &total, &before);
+  const long long per = (total + p.ctas - 1) / p.ctas;
+  const long long first = before + ((long long)h * p.tiles + tile) * ng;
+  const int c0 = (int)(first / per), c1 = (int)((first + ng - 1) / per);
+  if (c0 == c1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = r - tile * C::ROWS;
+  auto at = [&](int c) { return ((long long)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + rr; };
+  float top = -INFINITY, sum = 0.f;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.l_part[at(c)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float x = p.l_part[at(c)];
+    sum += x == -INFINITY ? 0.f : exp2f(x - top);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  constexpr int PER = D / 32;
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const float x = p.l_part[at(c)];
+    const float w = x == -INFINITY ? 0.f : exp2f(x - top) / sum;
+    const float *src = p.o_part + at(c) * D + lane;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[32 * e], acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) s_o[warp][lane + 32 * e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    const int c = 2 * threadIdx.x;
+    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] =
+        pack_bf16x2((s_o[0][c] + s_o[1][c]) + (s_o[2][c] + s_o[3][c]),
+                    (s_o[0][c + 1] + s_o[1][c + 1]) + (s_o[2][c + 1] + s_o[3][c + 1]));
+  }
+  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+constexpr int kCtas = 2 * 148;   // two per SM
+// Rows of a tile: 32 where more than 16 rows read a key/value head and O's
+// registers allow it (d <= 128), else 16.
+int row_tiles_mt(int R, int d) { return R > 16 && d <= 128 ? 2 : 1; }
+
+template <int D, int MT>
+int run_rows(const CacheArgs &a) {
+  using C = RowCfg<D, MT>;
+  RowParams p;
+  p.q = (const __nv_bfloat16 *)a.q;
+  p.k_cache = a.k_cache; p.v_cache = a.v_cache; p.k_scale = a.k_scale; p.v_scale = a.v_scale;
+  p.table = a.table; p.lens = a.lens;
+  p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
+  p.o_part = (float *)a.ws;
+  p.l_part = p.o_part + (size_t)kCtas * 2 * C::ROWS * D;
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq;
+  p.R = a.Hq / a.Hkv * a.Nq;
+  p.tiles = (p.R + C::ROWS - 1) / C::ROWS;
+  p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;
+  p.num_pages = a.num_pages; p.max_pages = a.max_pages;
+  p.causal = a.causal; p.ctas = kCtas;
+  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  p.err = a.err;
+  auto kern = fwd_cache_rows_kernel<D, MT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return 5;
+  kern<<<kCtas, kWarps * 32, C::SMEM, a.stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return 5;
+  const long long rows = (long long)a.B * a.Hq * a.Nq;
+  fwd_cache_merge_kernel<D, MT><<<(unsigned)rows, 128, 0, a.stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 
 }  // namespace
 
-size_t fwd_cache_ws_bytes(int, int, int, int, int) { return 0; }
+size_t fwd_cache_ws_bytes(int, int Hq, int Hkv, int Nq, int d) {
+  const double R = (double)(Hq / Hkv) * Nq;
+  const int rows = 16 * row_tiles_mt(R > 32.0 ? 32 : (int)R, d);
+  return (size_t)kCtas * 2 * rows * (d + 1) * 4;
+}
 
 int launch_fwd_cache(const CacheArgs &a) {
-  if (a.Hq > 65535 || a.B > 65535) return 2;
-  const dim3 grid((unsigned)a.Nq, (unsigned)a.Hq, (unsigned)a.B);
+  const double R = (double)(a.Hq / a.Hkv) * a.Nq;
+  if (R > 2147483647.0) return 2;
+  const int mt = row_tiles_mt(R > 32.0 ? 32 : (int)R, a.d);
+  if (a.Hkv * ((R + 16 * mt - 1) / (16 * mt)) > 2147483647.0) return 2;
   switch (a.d) {
-    case 64: fwd_cache_row_kernel<64><<<grid, 128, 0, a.stream>>>(a); break;
-    case 128: fwd_cache_row_kernel<128><<<grid, 128, 0, a.stream>>>(a); break;
-    case 256: fwd_cache_row_kernel<256><<<grid, 128, 0, a.stream>>>(a); break;
+    case 64: return mt == 2 ? run_rows<64, 2>(a) : run_rows<64, 1>(a);
+    case 128: return mt == 2 ? run_rows<128, 2>(a) : run_rows<128, 1>(a);
+    case 256: return run_rows<256, 1>(a);
     default: return 2;
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 
 }  // namespace fa

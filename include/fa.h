@@ -405,7 +405,8 @@ int fa_cache_read_f32(const void *k_cache, const void *v_cache, const float *k_s
  * sequence; causal == 0: every key.  A query that sees no key gets O = 0,
  * L = -inf.  Slots behind a sequence's length may hold anything.
  * Scores, the softmax statistics and O are float32; the codes enter the
- * matrix instructions exactly, the weights exp(s - m) rounded once to 11 bits.
+ * matrix instructions exactly.  The weights exp(s - m) * v_scale are rounded
+ * once to 11 bits, those below 2^-26 of a row's largest to steps of 2^-36 of it.
  * k_scale, v_scale: finite and > 0, as fa_cache_append writes them.
  *
  * workspace: fa_fwd_cache_workspace_size(...) bytes, 256-byte aligned

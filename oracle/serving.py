@@ -124,9 +124,11 @@ def cache_tokens(cache, scale, table_b, n, page):
 
 
 def cache_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, page, scale, causal):
-    """(O, L, W) float64: W[b, h, i, c] = sum_j p_j |v_jc|, the size of the
-    terms O is summed from; tokens on pages out of range are hidden.  Also the
-    largest scale * sum |q k| of each row, for error bounds: A [B, Hq, Nq]."""
+    """(O, L, W, A, U) float64; tokens on pages out of range are hidden.  For
+    error bounds: W[b, h, i, c] = sum_j p_j |v_jc|, the size of the terms O is
+    summed from; A[b, h, i], the largest scale * sum |q k| of a row; and
+    U[b, h, i, c] = max_j (p_j sv_j) * sum_j |code_jc|, what O would be off by
+    were every weight p_j sv_j off by as much as the largest."""
     q = np.asarray(q, np.float64)
     B, Hq, Nq, d = q.shape
     Hkv = k_cache.shape[1]
@@ -134,12 +136,14 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, page, sc
     w = np.zeros(q.shape)
     lse = np.full((B, Hq, Nq), -np.inf)
     amp = np.zeros((B, Hq, Nq))
+    unit = np.zeros(q.shape)
     for b in range(B):
         n = max(0, min(int(lens[b]), len(table[b]) * page))
         if n == 0:
             continue
         k = cache_tokens(k_cache, k_scale, table[b], n, page)
         v = cache_tokens(v_cache, v_scale, table[b], n, page)
+        sv = np.stack([v_scale[int(table[b][j // page]) % v_scale.shape[0]] for j in range(n)], 1)
         there = np.array([0 <= int(table[b][j // page]) < k_cache.shape[0] for j in range(n)])
         for h in range(Hq):
             hk = h // (Hq // Hkv)
@@ -157,4 +161,5 @@ def cache_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, page, sc
                 p = e / e.sum()
                 o[b, h, i] = p @ vv
                 w[b, h, i] = p @ np.abs(vv)
-    return o, lse, w, amp
+                unit[b, h, i] = (p * sv[hk][see]).max() * (np.abs(vv) / sv[hk][see][:, None]).sum(0)
+    return o, lse, w, amp, unit

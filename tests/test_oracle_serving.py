@@ -124,18 +124,18 @@ def test_cache_attention_equals_dense():
         S.cache_append(x[k], *c, table, [0], None, 16)
         caches.append(c)
     q = rng.normal(size=(1, 4, 3, 8))
-    o, lse, w, amp = S.cache_attention(q, caches[0][0], caches[1][0], caches[0][1], caches[1][1], table, [50],
+    o, lse, w, amp, unit = S.cache_attention(q, caches[0][0], caches[1][0], caches[0][1], caches[1][1], table, [50],
                                        16, 0.3, True)
     k = S.cache_tokens(*caches[0], table[0], 50, 16)[None]
     v = S.cache_tokens(*caches[1], table[0], 50, 16)[None]
     o_ref, l_ref = oracle.forward(q, k, v, 0.3, True, 47)
     assert np.allclose(o, o_ref, atol=1e-12) and np.allclose(lse, l_ref, atol=1e-12)
-    assert (w >= np.abs(o) - 1e-12).all() and (amp > 0).all()
+    assert (w >= np.abs(o) - 1e-12).all() and (unit >= w - 1e-12).all() and (amp > 0).all()
 
 
 def test_cache_attention_rows_without_keys():
     c, s = np.full((1, 1, 16, 4), 0x38, np.uint8), np.ones((1, 1))
-    o, lse, _, _ = S.cache_attention(np.ones((2, 1, 3, 4)), c, c, s, s, [[0], [0]], [2, 0], 16, 1.0, True)
+    o, lse, _, _, _ = S.cache_attention(np.ones((2, 1, 3, 4)), c, c, s, s, [[0], [0]], [2, 0], 16, 1.0, True)
     assert (o[0, 0, 0] == 0).all() and lse[0, 0, 0] == -np.inf      # length 2, query 0 of 3 stands before it
     assert np.allclose(o[0, 0, 1:], 1.0) and (lse[1] == -np.inf).all() and (o[1] == 0).all()
 
@@ -146,5 +146,5 @@ def test_pages_out_of_range_are_left_out(bad):
     before = c.copy()
     S.cache_append(np.ones((1, 1, 20, 4)), c, s, [[bad, 1]], [0], None, 16)
     assert np.array_equal(c[0], before[0])
-    o, lse, _, _ = S.cache_attention(np.ones((1, 1, 1, 4)), c, c, s, s, [[bad, 1]], [20], 16, 1.0, False)
+    o, lse, _, _, _ = S.cache_attention(np.ones((1, 1, 1, 4)), c, c, s, s, [[bad, 1]], [20], 16, 1.0, False)
     assert np.allclose(lse, 4.0 + np.log(4))
