@@ -98,7 +98,7 @@ def lib():
             fn.restype = I
         L.fa_fwd_cache.argtypes = [P] * 10 + [I] * 8 + [F, I, P]
         L.fa_fwd_cache.restype = I
-        L.fa_fwd_cache_workspace_size.argtypes = [I] * 5
+        L.fa_fwd_cache_workspace_size.argtypes = [I] * 7
         L.fa_fwd_cache_workspace_size.restype = S
         L.fa_device_status.argtypes = [P]
         L.fa_device_status.restype = I
@@ -236,8 +236,8 @@ def fa_cache_read_f32(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, 
                                    Hkv, N, d, page, num_pages, max_pages, stream)
 
 
-def fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d):
-    return int(lib().fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d))
+def fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages):
+    return int(lib().fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages))
 
 
 def fa_fwd_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, ws, B, Hq, Hkv,
@@ -296,6 +296,13 @@ def _check_cuda(where, q, *others):
     library launches on the current device, which the wrappers set to q's
     (``_on``), so a tensor on another GPU would be read by kernels running on
     the wrong one."""
+    dev = q.device
+    if q.is_cuda and q.is_contiguous():
+        for t in others:
+            if t.device != dev or not t.is_contiguous():
+                break
+        else:
+            return
     for t in (q,) + others:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{where}: inputs must be contiguous CUDA tensors")
@@ -325,6 +332,21 @@ def _workspace(where, workspace, B, Hq, Nq, d, device):
         raise ValueError(f"{where}: workspace must be on q's device ({device}); "
                          f"got {workspace.device}")
     return workspace
+
+
+def _call(fn, name, t, *args):
+    """fn(*args, stream) on t's device and that device's current stream; raises
+    FaError.  The context switch and the stream object are skipped where the
+    device is current already: a decode step's calls are as short as this."""
+    import torch
+    dev = t.device.index
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != FA_OK:
+        raise FaError(st, name)
 
 
 def _shape(q, k):
@@ -489,7 +511,7 @@ def rope_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=
             float(mscale.value))
 
 
-def _rope(where, q, k, positions, freqs, mscale, interleaved, out, fn_bf16, fn_f32):
+def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
     import torch
     if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{where}: q must be [B, Hq, N, d], bfloat16 or float32")
@@ -511,17 +533,15 @@ def _rope(where, q, k, positions, freqs, mscale, interleaved, out, fn_bf16, fn_f
         ko = None if k is None else torch.empty_like(k)
     else:
         qo, ko = out
-        for name, t, o in (("q", q, qo), ("k", k, ko)):
+        for t, o in ((q, qo), (k, ko)):
             if (o is None) != (t is None) or (t is not None and (o.shape != t.shape
                                                                  or o.dtype != t.dtype)):
                 raise ValueError(f"{where}: out must be shaped and typed like (q, k)")
     _check_cuda(where, q, positions, freqs, qo, *(() if k is None else (k, ko)))
-    fn = fn_bf16 if q.dtype == torch.bfloat16 else fn_f32
-    with _on(q):
-        _check(fn(q.data_ptr(), 0 if k is None else k.data_ptr(), qo.data_ptr(),
-                  0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(), B, Hq,
-                  Hkv, N, d, 2 * freqs.shape[0], per_batch, interleaved, float(mscale),
-                  _stream(q)), fn.__name__)
+    name = name if q.dtype == torch.bfloat16 else name + "_f32"
+    _call(getattr(lib(), name), name, q, q.data_ptr(), 0 if k is None else k.data_ptr(),
+          qo.data_ptr(), 0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
+          B, Hq, Hkv, N, d, 2 * freqs.shape[0], int(per_batch), int(interleaved), float(mscale))
     return qo, ko
 
 
@@ -530,42 +550,45 @@ def rope(q, k, positions, freqs, mscale=1.0, interleaved=False, out=None):
     may be None), bfloat16 or float32, in one launch (fa_rope, fa_rope_f32).
     positions: int32 [B, N] or [N]; freqs, mscale: ``rope_freqs``.  out=(q, k)
     turns in place."""
-    return _rope("rope", q, k, positions, freqs, mscale, interleaved, out, fa_rope, fa_rope_f32)
+    return _rope("rope", q, k, positions, freqs, mscale, interleaved, out, "fa_rope")
 
 
 def rope_backward(dq, dk, positions, freqs, mscale=1.0, interleaved=False, out=None):
     """Gradients of ``rope``'s inputs from those of its outputs (fa_rope_bwd,
     fa_rope_bwd_f32); dk may be None."""
-    return _rope("rope_backward", dq, dk, positions, freqs, mscale, interleaved, out, fa_rope_bwd,
-                 fa_rope_bwd_f32)
+    return _rope("rope_backward", dq, dk, positions, freqs, mscale, interleaved, out,
+                 "fa_rope_bwd")
 
 
-def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, d, *arrays):
-    """The cache's tensors against B, Hkv, d; `arrays`: (name, int32 [B] tensor
-    or None) pairs.  Returns (page, num_pages, max_pages)."""
+def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, d, *more):
+    """The cache's tensors against B, Hkv, d.  `more`: (name, int32 [B] tensor
+    or None) pairs, or tensors whose place alone is checked.  Returns (page,
+    num_pages, max_pages)."""
     import torch
-    f8 = (torch.float8_e4m3fn, torch.uint8)
-    if (k_cache.dim() != 4 or k_cache.dtype not in f8 or k_cache.shape[1] != Hkv
-            or k_cache.shape[3] != d or v_cache.shape != k_cache.shape
-            or v_cache.dtype not in f8):
+    f8 = (torch.uint8, torch.float8_e4m3fn)
+    shape = k_cache.shape
+    if (len(shape) != 4 or shape[1] != Hkv or shape[3] != d or v_cache.shape != shape
+            or k_cache.dtype not in f8 or v_cache.dtype not in f8):
         raise ValueError(f"{where}: k_cache and v_cache must be E4M3 [num_pages, Hkv, page, d]")
-    num_pages, _, page, _ = k_cache.shape
+    num_pages, _, page, _ = shape
     shape = (num_pages, Hkv)
     if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype != torch.float32
             or v_scale.dtype != torch.float32):
         raise ValueError(f"{where}: k_scale and v_scale must be float32 [num_pages, Hkv]")
-    if (block_table.dim() != 2 or block_table.shape[0] != B
-            or block_table.dtype != torch.int32):
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B or block_table.dtype != torch.int32:
         raise ValueError(f"{where}: block_table must be int32 [B, max_pages]")
-    present = []
-    for name, t in arrays:
-        if t is None:
-            continue
-        if t.shape != (B,) or t.dtype != torch.int32:
-            raise ValueError(f"{where}: {name} must be int32 [B]")
-        present.append(t)
-    _check_cuda(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, *present)
-    return page, num_pages, block_table.shape[1]
+    place = [k_cache, v_cache, k_scale, v_scale, block_table]
+    for x in more:
+        if isinstance(x, tuple):
+            name, x = x
+            if x is None:
+                continue
+            if x.shape != (B,) or x.dtype != torch.int32:
+                raise ValueError(f"{where}: {name} must be int32 [B]")
+        place.append(x)
+    _check_cuda(where, ref, *place)
+    return page, num_pages, shape[1]
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None):
@@ -583,14 +606,12 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, c
         raise ValueError("cache_append: start must be int32 [B]")
     page, num_pages, max_pages = _check_cache("cache_append", k, k_cache, v_cache, k_scale, v_scale,
                                               block_table, B, Hkv, d, ("start", start),
-                                              ("count", count))
-    _check_cuda("cache_append", k, v)
-    fn = fa_cache_append if k.dtype == torch.bfloat16 else fa_cache_append_f32
-    with _on(k):
-        _check(fn(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                  k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-                  start.data_ptr(), 0 if count is None else count.data_ptr(), B, Hkv, T, d, page,
-                  num_pages, max_pages, _stream(k)), fn.__name__)
+                                              ("count", count), v)
+    name = "fa_cache_append" if k.dtype == torch.bfloat16 else "fa_cache_append_f32"
+    _call(getattr(lib(), name), name, k, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+          start.data_ptr(), 0 if count is None else count.data_ptr(), B, Hkv, T, d, page,
+          num_pages, max_pages)
 
 
 def cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, N, dtype=None):
@@ -610,11 +631,10 @@ def cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, N, dtype=N
                                               v_scale, block_table, B, Hkv, d, ("lens", lens))
     k = torch.empty(B, Hkv, N, d, device=k_cache.device, dtype=dtype)
     v = torch.empty_like(k)
-    fn = fa_cache_read if dtype == torch.bfloat16 else fa_cache_read_f32
-    with _on(k_cache):
-        _check(fn(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  block_table.data_ptr(), lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, N,
-                  d, page, num_pages, max_pages, _stream(k_cache)), fn.__name__)
+    name = "fa_cache_read" if dtype == torch.bfloat16 else "fa_cache_read_f32"
+    _call(getattr(lib(), name), name, k_cache, k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+          k.data_ptr(), v.data_ptr(), B, Hkv, N, d, page, num_pages, max_pages)
     return k, v
 
 
@@ -635,7 +655,7 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     page, num_pages, max_pages = _check_cache("forward_cache", q, k_cache, v_cache, k_scale,
                                               v_scale, block_table, B, Hkv, d, ("lens", lens))
     scale = d ** -0.5 if scale is None else float(scale)
-    need = fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d)
+    need = int(lib().fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages))
     if workspace is None:
         workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
     elif (not workspace.is_cuda or not workspace.is_contiguous()
@@ -647,11 +667,9 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
                          f"got {workspace.device}")
     o = torch.empty_like(q)
     L = torch.empty(B, Hq, Nq, device=q.device, dtype=torch.float32)
-    with _on(q):
-        _check(fa_fwd_cache(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-                            lens.data_ptr(), o.data_ptr(), L.data_ptr(),
-                            0 if workspace is None else workspace.data_ptr(), B, Hq, Hkv, Nq, d,
-                            page, num_pages, max_pages, scale, causal, _stream(q)),
-               "fa_fwd_cache")
+    _call(lib().fa_fwd_cache, "fa_fwd_cache", q, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+          lens.data_ptr(), o.data_ptr(), L.data_ptr(),
+          0 if workspace is None else workspace.data_ptr(), B, Hq, Hkv, Nq, d, page, num_pages,
+          max_pages, scale, int(causal))
     return o, L

@@ -34,12 +34,17 @@ unsigned *error_word(int dev) {
   return g_err_ptr[dev];
 }
 
+// Devices found to be compute capability 10.0 (looked up once).
+bool g_arch_ok[kMaxDevices] = {};
+
 int check_arch(int dev) {
+  if (g_arch_ok[dev]) return FA_OK;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return FA_ERR_CUDA;
-  return (major == 10 && minor == 0) ? FA_OK : FA_ERR_ARCH;
+  g_arch_ok[dev] = major == 10 && minor == 0;
+  return g_arch_ok[dev] ? FA_OK : FA_ERR_ARCH;
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }

@@ -176,10 +176,13 @@ FA_APPEND_ENTRY(fa_cache_append_f32, float, 1)
 FA_READ_ENTRY(fa_cache_read, void, 0)
 FA_READ_ENTRY(fa_cache_read_f32, float, 1)
 
-FA_EXPORT size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Nq <= 0) return 0;
-  if (d != 64 && d != 128 && d != 256) return 0;
-  return fa::fwd_cache_ws_bytes(B, Hq, Hkv, Nq, d);
+FA_EXPORT size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d, int page,
+                                             int max_pages) {
+  CacheArgs a;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.Nq = Nq; a.d = d; a.page = page; a.max_pages = max_pages;
+  a.num_pages = 1;
+  if (fa::check_cache(a, Nq) || Hq <= 0 || Hq % Hkv) return 0;
+  return fa::fwd_cache_ws_bytes(a);
 }
 
 FA_EXPORT int fa_fwd_cache(const void *q, const void *k_cache, const void *v_cache,
@@ -203,7 +206,7 @@ FA_EXPORT int fa_fwd_cache(const void *q, const void *k_cache, const void *v_cac
   if (Hq <= 0 || Hq % Hkv || !(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
   if ((double)B * Hq * Nq > 2147483647.0 || (double)B * Hq * Nq * d > 4.0e12)
     return FA_ERR_UNSUPPORTED;
-  const bool need_ws = fa::fwd_cache_ws_bytes(B, Hq, Hkv, Nq, d) > 0;
+  const bool need_ws = fa::fwd_cache_ws_bytes(a) > 0;
   if (need_ws && !workspace) return FA_ERR_INVALID_ARG;
   if (!fa::cache_aligned(a)) return FA_ERR_ALIGNMENT;
   if (need_ws && ((uintptr_t)workspace & 255u)) return FA_ERR_ALIGNMENT;

@@ -37,6 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kStep = 16;                       // tokens a warp takes at a time
 constexpr int kGranule = kWarps * kStep;
 constexpr int kRingBytes = 24 * 1024;           // per warp
+constexpr int kMaxCtas = 2 * 148;               // two per SM
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
 constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 
@@ -99,6 +100,15 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// Programmatic dependent launch: the next kernel of the stream may start; a
+// dependent kernel waits here until the one before it has ended.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 struct RowParams {
   const __nv_bfloat16 *q;
   const uint8_t *k_cache, *v_cache;
@@ -106,10 +116,10 @@ struct RowParams {
   const int *table, *lens;
   __nv_bfloat16 *o;
   float *lse;
-  float *o_part, *l_part;   // [grid][2][ROWS][D], [grid][2][ROWS] (base 2)
+  float *o_part, *l_part;   // [grid][2][prows][D], [grid][2][prows] (base 2)
   int B, Hq, Hkv, Nq, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
   int page_log2, num_pages, max_pages;
-  int causal, ctas;
+  int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
   float scale_log2;
   unsigned *err;
 };
@@ -157,6 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
   const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int units = p.Hkv * p.tiles;
+  launch_dependents();   // the merge kernel's CTAs may take their places
 
   // This CTA's run of the line, and the sequence it starts in.
   long long total, unused;
@@ -218,64 +229,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
     const int group = p.Hq / p.Hkv;
     const long long row_base = ((long long)b * p.Hq + (long long)h * group) * p.Nq;   // row 0 of q, o, lse
 
-    // ---- q: A fragments of halves, each row times a power of two
-    uint32_t qa[MT][C::CH][4];
-    float row_c[MT][2];        // scale * log2 e / that power of two
-    int lim[MT][2];            // keys [0, lim) visible
-    int lim_min = len;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = r0 + mt * 16 + g + 8 * e;
-        const bool live = r < p.R;
-        const __nv_bfloat16 *src = p.q + (row_base + (live ? r : 0)) * D + 4 * t;
-        uint2 raw[C::CH];
-        float mx = 0.f;
-#pragma unroll
-        for (int c = 0; c < C::CH; ++c) {
-          raw[c] = live ? *reinterpret_cast<const uint2 *>(src + 16 * c) : make_uint2(0u, 0u);
-          const uint32_t w[2] = {raw[c].x, raw[c].y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] << 16)));
-            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
-          }
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // mx in [2^k, 2^{k+1}); zero rows and exponents past float32's reach are cut off
-        const int k = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
-        const float up = __uint_as_float((uint32_t)(13 - k + 127) << 23);
-        row_c[mt][e] = p.scale_log2 * __uint_as_float((uint32_t)(k - 13 + 127) << 23);
-#pragma unroll
-        for (int c = 0; c < C::CH; ++c) {
-          qa[mt][c][e] = pack_half2(__uint_as_float(raw[c].x << 16) * up,
-                                    __uint_as_float(raw[c].x & 0xFFFF0000u) * up);
-          qa[mt][c][2 + e] = pack_half2(__uint_as_float(raw[c].y << 16) * up,
-                                        __uint_as_float(raw[c].y & 0xFFFF0000u) * up);
-        }
-        lim[mt][e] = !live ? 0 : (p.causal ? max(0, len - p.Nq + r % p.Nq + 1) : len);
-        if (live) lim_min = min(lim_min, lim[mt][e]);
-      }
-    }
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-
-    float o[MT][D / 8][4];
-    float m_s[MT][2], m_o[MT][2], l[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m_s[mt][e] = m_o[mt][e] = -INFINITY;
-        l[mt][e] = 0.f;
-      }
-    }
-
     // ---- pages: lane i holds page, sk and log2 sv of step 32 k + i
     const int steps = g1 - g0;
     const int *tab = p.table + (long long)b * p.max_pages;
@@ -328,6 +281,66 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       cp_async_commit();
     };
     for (int s = 0; s < C::STAGES - 1; ++s) issue(s);
+
+    // ---- q: A fragments of halves, each row times a power of two
+    uint32_t qa[MT][C::CH][4];
+    float row_c[MT][2];        // scale * log2 e / that power of two
+    int lim[MT][2];            // keys [0, lim) visible
+    int lim_min = len;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + mt * 16 + g + 8 * e;
+        const bool live = r < p.R;
+        const __nv_bfloat16 *src = p.q + (row_base + (live ? r : 0)) * D + 4 * t;
+        uint2 raw[C::CH];
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c)
+          raw[c] = live ? *reinterpret_cast<const uint2 *>(src + 16 * c) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) {
+          const uint32_t w[2] = {raw[c].x, raw[c].y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] << 16)));
+            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // mx in [2^k, 2^{k+1}); zero rows and exponents past float32's reach are cut off
+        const int k = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
+        const float up = __uint_as_float((uint32_t)(13 - k + 127) << 23);
+        row_c[mt][e] = p.scale_log2 * __uint_as_float((uint32_t)(k - 13 + 127) << 23);
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) {
+          qa[mt][c][e] = pack_half2(__uint_as_float(raw[c].x << 16) * up,
+                                    __uint_as_float(raw[c].x & 0xFFFF0000u) * up);
+          qa[mt][c][2 + e] = pack_half2(__uint_as_float(raw[c].y << 16) * up,
+                                        __uint_as_float(raw[c].y & 0xFFFF0000u) * up);
+        }
+        lim[mt][e] = !live ? 0 : (p.causal ? max(0, len - p.Nq + r % p.Nq + 1) : len);
+        if (live) lim_min = min(lim_min, lim[mt][e]);
+      }
+    }
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+
+    float o[MT][D / 8][4];
+    float m_s[MT][2], m_o[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_s[mt][e] = m_o[mt][e] = -INFINITY;
+        l[mt][e] = 0.f;
+      }
+    }
 
     for (int s = 0; s < steps; ++s) {
       cp_async_wait<C::STAGES - 2>();
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
         }
     __syncthreads();
     const bool final = g0 == 0 && g1 == ng;
-    const long long part = ((long long)blockIdx.x * 2 + (g0 == 0 ? 1 : 0)) * C::ROWS;
+    const long long part = ((long long)blockIdx.x * 2 + (g0 == 0 ? 1 : 0)) * p.prows;
     const int rows = min(C::ROWS, p.R - r0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), c4 = i - r * (D / 4);
@@ -549,13 +562,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
   }
 }
 
+template <int PER>
+__device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
+  if constexpr (PER == 2) {
+    const float2 x = *reinterpret_cast<const float2 *>(src);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; e += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(src + e);
+      v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
+    }
+  }
+}
+
 // Joins the pieces of the units that several CTAs covered, one CTA per query
 // row; rows of sequences without tokens become O = 0, L = -inf.
 template <int D, int MT>
 __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p) {
   using C = RowCfg<D, MT>;
   __shared__ long long s_red[4];
-  __shared__ float s_o[4][D];
+  __shared__ float s_o[4][D], s_w[kMaxCtas];
   const long long row = blockIdx.x;
   const int b = (int)(row / ((long long)p.Hq * p.Nq));
   const int hr = (int)(row - (long long)b * p.Hq * p.Nq);   // row within the sequence
@@ -563,6 +590,7 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p)
   const int ng = granules_of(p, b);
   __nv_bfloat16 *dst = p.o + row * D;
   if (ng == 0) {
+    wait_for_primary();
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
     if (threadIdx.x == 0) {
       p.lse[row] = -INFINITY;
@@ -575,32 +603,49 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p)
   const long long per = (total + p.ctas - 1) / p.ctas;
   const long long first = before + ((long long)h * p.tiles + tile) * ng;
   const int c0 = (int)(first / per), c1 = (int)((first + ng - 1) / per);
+  // every CTA waits, so that what follows in the stream finds o and lse whole
+  wait_for_primary();
   if (c0 == c1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = r - tile * C::ROWS;
-  auto at = [&](int c) { return ((long long)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + rr; };
+  const int n = c1 - c0 + 1;
+  auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
+  // every warp forms the same maximum and sum; each keeps a quarter of the weights
   float top = -INFINITY, sum = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.l_part[at(c)]);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float x = p.l_part[at(c)];
-    sum += x == -INFINITY ? 0.f : exp2f(x - top);
+  for (int i = lane; i < n; i += 32) {
+    const float x = p.l_part[at(i)];
+    const float w = x == -INFINITY ? 0.f : exp2f(x - top);
+    sum += w;
+    if ((i & 3) == warp) s_w[i] = w;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  __syncwarp();
+  // warp w adds pieces w, w + 4, ...: eight loads in flight
   constexpr int PER = D / 32;
   float acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const float x = p.l_part[at(c)];
-    const float w = x == -INFINITY ? 0.f : exp2f(x - top) / sum;
-    const float *src = p.o_part + at(c) * D + lane;
+  const float *src = p.o_part + lane * PER;
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += 32) {
+    float v[8][PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[32 * e], acc[e]);
+    for (int k = 0; k < 8; ++k)
+      if (i0 + 4 * k < n) load_floats<PER>(src + at(i0 + 4 * k) * D, v[k]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + 4 * k < n) {
+        const float w = s_w[i0 + 4 * k];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+      }
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) s_o[warp][lane + 32 * e] = acc[e];
+  for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e] * inv;
   __syncthreads();
   if (threadIdx.x < D / 2) {
     const int c = 2 * threadIdx.x;
@@ -611,13 +656,31 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p)
   if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
-constexpr int kCtas = 2 * 148;   // two per SM
 // Rows of a tile: 32 where more than 16 rows read a key/value head and O's
 // registers allow it (d <= 128), else 16.
-int row_tiles_mt(int R, int d) { return R > 16 && d <= 128 ? 2 : 1; }
+int tile_rows(double R, int d) { return R > 16 && d <= 128 ? 32 : 16; }
+
+// What the host knows of the work: rows, tiles, CTAs (two per SM, fewer when
+// the block table has room for fewer granules).
+struct RowPlan {
+  double R;
+  int rows, prows;
+  long long tiles;
+  int ctas;
+};
+RowPlan plan_of(const CacheArgs &a) {
+  RowPlan x;
+  x.R = (double)(a.Hq / a.Hkv) * a.Nq;
+  x.rows = tile_rows(x.R, a.d);
+  x.prows = x.R < x.rows ? (int)x.R : x.rows;
+  x.tiles = (long long)((x.R + x.rows - 1) / x.rows);
+  const double most = (double)a.B * a.Hkv * x.tiles * (((long long)a.max_pages * a.page + kGranule - 1) / kGranule);
+  x.ctas = most < kMaxCtas ? (int)most : kMaxCtas;
+  return x;
+}
 
 template <int D, int MT>
-int run_rows(const CacheArgs &a) {
+int run_rows(const CacheArgs &a, const RowPlan &x) {
   using C = RowCfg<D, MT>;
   RowParams p;
   p.q = (const __nv_bfloat16 *)a.q;
@@ -625,42 +688,50 @@ int run_rows(const CacheArgs &a) {
   p.table = a.table; p.lens = a.lens;
   p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
   p.o_part = (float *)a.ws;
-  p.l_part = p.o_part + (size_t)kCtas * 2 * C::ROWS * D;
+  p.l_part = p.o_part + (size_t)x.ctas * 2 * x.prows * D;
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq;
-  p.R = a.Hq / a.Hkv * a.Nq;
-  p.tiles = (p.R + C::ROWS - 1) / C::ROWS;
+  p.R = (int)x.R;
+  p.tiles = (int)x.tiles;
   p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;
   p.num_pages = a.num_pages; p.max_pages = a.max_pages;
-  p.causal = a.causal; p.ctas = kCtas;
+  p.causal = a.causal; p.ctas = x.ctas; p.prows = x.prows;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.err = a.err;
   auto kern = fwd_cache_rows_kernel<D, MT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return 5;
-  kern<<<kCtas, kWarps * 32, C::SMEM, a.stream>>>(p);
+  kern<<<x.ctas, kWarps * 32, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
-  const long long rows = (long long)a.B * a.Hq * a.Nq;
-  fwd_cache_merge_kernel<D, MT><<<(unsigned)rows, 128, 0, a.stream>>>(p);
+  // The merge kernel is launched while the main one runs: its CTAs find their
+  // pieces, then wait for the main kernel's end.
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq * a.Nq), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = a.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, MT>, p) != cudaSuccess) return 5;
   return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 
 }  // namespace
 
-size_t fwd_cache_ws_bytes(int, int Hq, int Hkv, int Nq, int d) {
-  const double R = (double)(Hq / Hkv) * Nq;
-  const int rows = 16 * row_tiles_mt(R > 32.0 ? 32 : (int)R, d);
-  return (size_t)kCtas * 2 * rows * (d + 1) * 4;
+size_t fwd_cache_ws_bytes(const CacheArgs &a) {
+  const RowPlan x = plan_of(a);
+  return (size_t)x.ctas * 2 * x.prows * (a.d + 1) * 4;
 }
 
 int launch_fwd_cache(const CacheArgs &a) {
-  const double R = (double)(a.Hq / a.Hkv) * a.Nq;
-  if (R > 2147483647.0) return 2;
-  const int mt = row_tiles_mt(R > 32.0 ? 32 : (int)R, a.d);
-  if (a.Hkv * ((R + 16 * mt - 1) / (16 * mt)) > 2147483647.0) return 2;
+  const RowPlan x = plan_of(a);
+  if (x.R > 2147483647.0 || (double)a.Hkv * x.tiles > 2147483647.0) return 2;
+  const bool wide = x.rows == 32;
   switch (a.d) {
-    case 64: return mt == 2 ? run_rows<64, 2>(a) : run_rows<64, 1>(a);
-    case 128: return mt == 2 ? run_rows<128, 2>(a) : run_rows<128, 1>(a);
-    case 256: return run_rows<256, 1>(a);
+    case 64: return wide ? run_rows<64, 2>(a, x) : run_rows<64, 1>(a, x);
+    case 128: return wide ? run_rows<128, 2>(a, x) : run_rows<128, 1>(a, x);
+    case 256: return run_rows<256, 1>(a, x);
     default: return 2;
   }
 }

@@ -110,7 +110,7 @@ struct CacheArgs {
 int launch_cache_append(const CacheArgs &a);
 int launch_cache_read(const CacheArgs &a);
 int launch_fwd_cache(const CacheArgs &a);
-size_t fwd_cache_ws_bytes(int B, int Hq, int Hkv, int Nq, int d);
+size_t fwd_cache_ws_bytes(const CacheArgs &a);   // by B, Hq, Hkv, Nq, d, page, max_pages
 
 // Argument checks and per-call device set-up shared by the C entry points
 // (fa_status codes): size/scale rules, then current device, architecture and

@@ -413,7 +413,7 @@ int fa_cache_read_f32(const void *k_cache, const void *v_cache, const float *k_s
  * (NULL when that is 0); contents ignored on entry and clobbered, so calls
  * that may overlap on the GPU (two graphs, two streams) need one each.
  */
-size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d, int page, int max_pages);
 int fa_fwd_cache(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                  const float *v_scale, const int *block_table, const int *lens, void *o, float *lse,
                  void *workspace, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages,

@@ -112,12 +112,12 @@ def test_forward_cache_argument_errors():
     for i in range(9):
         off = 8 if i in (0, 1, 2, 7) else 2
         assert call(ptrs=tuple(FAKE + off if j == i else FAKE for j in range(10))) == F.FA_ERR_ALIGNMENT
-    if F.fa_fwd_cache_workspace_size(2, 4, 2, 8, 64):
-        assert call(ptrs=(FAKE,) * 9 + (0,)) == F.FA_ERR_INVALID_ARG
-        assert call(ptrs=(FAKE,) * 9 + (FAKE + 64,)) == F.FA_ERR_ALIGNMENT
-    assert F.fa_fwd_cache_workspace_size(0, 4, 2, 8, 64) == 0
-    assert F.fa_fwd_cache_workspace_size(1, 4, 3, 8, 64) == 0
-    assert F.fa_fwd_cache_workspace_size(1, 4, 2, 8, 96) == 0
+    assert F.fa_fwd_cache_workspace_size(2, 4, 2, 8, 64, 64, 9) > 0
+    assert call(ptrs=(FAKE,) * 9 + (0,), max_pages=99) == F.FA_ERR_INVALID_ARG
+    assert call(ptrs=(FAKE,) * 9 + (FAKE + 64,), max_pages=99) == F.FA_ERR_ALIGNMENT
+    for bad in ((0, 4, 2, 8, 64, 64, 9), (1, 4, 3, 8, 64, 64, 9), (1, 4, 2, 8, 96, 64, 9), (1, 4, 2, 8, 64, 24, 9),
+                (1, 4, 2, 8, 64, 64, 0), (1, 0, 2, 8, 64, 64, 9)):
+        assert F.fa_fwd_cache_workspace_size(*bad) == 0
 
 
 def _cache(idx=0, H=2, d=64, pages=9, page=16, B=2):

@@ -85,8 +85,8 @@ def test_rope(c, backward):
     fn = F.rope_backward if backward else F.rope
     qg, kg = q.cuda(), None if k is None else k.cuda()
     outs = fn(qg, kg, pos.cuda(), freqs, ms, inter)
-    again = fn(qg.clone(), None if k is None else kg.clone(), pos.cuda(), freqs, ms, inter,
-               out=(qg, kg))                       # in place
+    again = fn(qg, kg, pos.cuda(), freqs, ms, inter, out=(qg, kg))   # in place
+    assert again[0] is qg and again[1] is kg
     torch.cuda.synchronize()
     assert F.fa_device_status() == F.FA_OK
     ms32 = float(np.float32(ms))
