@@ -34,8 +34,8 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStep = 16;                       // tokens a warp takes at a time
-constexpr int kGranule = kWarps * kStep;
+constexpr int kSub = 16;                        // tokens of a subtile (one page's, or part of it)
+constexpr int kGranule = kWarps * kSub;
 constexpr int kRingBytes = 24 * 1024;           // per warp
 constexpr int kMaxCtas = 2 * 148;               // two per SM
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
@@ -45,21 +45,32 @@ template <int D, int MT>
 struct RowCfg {
   static constexpr int ROWS = 16 * MT;
   static constexpr int CH = D / 16;             // 16-byte chunks of a token
-  static constexpr int STAGE = 2 * kStep * D;   // K then V codes of a step
+  // Subtiles a warp takes at a time: two where the registers allow (their
+  // scores beside q and O), which halves the work around them.
+  static constexpr int NS = D * MT <= 128 ? 2 : 1;
+  static constexpr int TILE = kSub * D;         // K or V codes of a subtile
+  static constexpr int STAGE = 2 * NS * TILE;
   static constexpr int STAGES = kRingBytes / STAGE;
-  static constexpr int OFF_META = kWarps * kRingBytes;
-  static constexpr int OFF_STAT = OFF_META + kWarps * STAGES * 16;
+  static constexpr int OFF_SCALE = kWarps * kRingBytes;                  // [warp][stage][NS] (sk, sv)
+  static constexpr int OFF_STAT = OFF_SCALE + kWarps * STAGES * NS * 8;  // [warp][ROWS]
   static constexpr int SMEM = OFF_STAT + kWarps * ROWS * 4;
   static_assert(ROWS * D * 4 <= kRingBytes, "a warp's O fits in its ring");
   static_assert(STAGES >= 3, "ring depth");
 };
 
-// Byte offset of 16-byte chunk c of token r in a step's tile: chunks are
+// Byte offset of 16-byte chunk c of token r in a subtile's tile: chunks are
 // permuted so that eight tokens' chunk c lie in eight different bank groups.
 template <int D>
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   else return r * D + ((c ^ (r & 7)) << 4);
+}
+// The same for chunk 32 i + lane of the tile in token order, `first` being
+// tile_at of chunk `lane`: a warp-wide copy moves 512 bytes.
+template <int D>
+__device__ __forceinline__ uint32_t tile_chunk(uint32_t first, int i) {
+  constexpr int RPI = 512 / D;   // tokens of one copy
+  return 512 * i + (D == 64 ? first : first ^ (((i * RPI) & 7) << 4));
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
@@ -68,6 +79,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool l
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0)
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -129,88 +144,77 @@ __device__ __forceinline__ int granules_of(const RowParams &p, int b) {
   return (min(max(n, 0), p.max_pages << p.page_log2) + kGranule - 1) / kGranule;
 }
 
-// Sum over the block of a value per thread (every thread gets it).
-__device__ __forceinline__ long long block_sum(long long v, long long *s_red) {
-  const int nw = blockDim.x >> 5;
+__device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long t = 0;
-  for (int w = 0; w < nw; ++w) t += s_red[w];
-  return t;
+  return v;
 }
 
 // The line of granules: sequences in order, each with Hkv * tiles units of
-// granules_of(b).  Gives the total and the granules before sequence b.
-__device__ __forceinline__ void line_of(const RowParams &p, int b, long long *s_red, long long *total,
-                                        long long *before) {
+// granules_of(b).  Granules of all sequences, and of those before sequence b
+// (of one unit each); every warp forms them for itself.
+__device__ __forceinline__ void line_of(const RowParams &p, int b, long long *total, long long *before) {
+  const int lane = threadIdx.x & 31;
   long long all = 0, pre = 0;
-  for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+  for (int i = lane; i < p.B; i += 32) {
     const int n = granules_of(p, i);
     all += n;
     if (i < b) pre += n;
   }
-  const long long units = (long long)p.Hkv * p.tiles;
-  *total = block_sum(all, s_red) * units;
-  *before = b > 0 ? block_sum(pre, s_red) * units : 0;
+  *total = warp_sum(all);
+  *before = b > 0 ? warp_sum(pre) : 0;
+}
+
+// The sequence that holds granule `pos` of the line cut to one unit a
+// sequence (pos < the total), and the granules before it.
+__device__ __forceinline__ int sequence_at(const RowParams &p, long long pos, long long *before) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  for (int i0 = 0;; i0 += 32) {
+    const int n = i0 + lane < p.B ? granules_of(p, i0 + lane) : 0;
+    long long inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    inc += base;
+    const unsigned past = __ballot_sync(0xffffffffu, pos < inc);
+    if (past || i0 + 32 >= p.B) {
+      const int at = past ? __ffs(past) - 1 : 31;
+      *before = __shfl_sync(0xffffffffu, inc - n, at);
+      return min(i0 + at, p.B - 1);
+    }
+    base = __shfl_sync(0xffffffffu, inc, 31);
+  }
 }
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const RowParams p) {
   using C = RowCfg<D, MT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_red[kWarps];
-  __shared__ int s_b;
-  __shared__ long long s_before;
   const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int units = p.Hkv * p.tiles;
   launch_dependents();   // the merge kernel's CTAs may take their places
 
   // This CTA's run of the line, and the sequence it starts in.
-  long long total, unused;
-  line_of(p, 0, s_red, &total, &unused);
-  const long long per = (total + p.ctas - 1) / p.ctas;
-  long long pos = per * blockIdx.x;
-  const long long end = min(total, pos + per);
-  if (pos >= end) return;
+  long long total, pos, end, b_first;
+  line_of(p, 0, &total, &b_first);
+  total *= units;
   {
-    long long base = 0;   // granules of the sequences before this chunk of 128
-    for (int i0 = 0; i0 < p.B; i0 += blockDim.x) {
-      const int i = i0 + (int)threadIdx.x;
-      const long long n = i < p.B ? (long long)granules_of(p, i) * units : 0;
-      long long inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += o;
-      }
-      __syncthreads();
-      if (lane == 31) s_red[warp] = inc;
-      __syncthreads();
-      long long pre = base, chunk = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) pre += s_red[w];
-        chunk += s_red[w];
-      }
-      inc += pre;
-      if (pos >= inc - n && pos < inc) {
-        s_b = i;
-        s_before = inc - n;
-      }
-      base += chunk;
-      if (base > pos) break;   // uniform: found in this chunk
-    }
-    __syncthreads();
+    const long long per = (total + p.ctas - 1) / p.ctas;
+    pos = per * blockIdx.x;
+    end = min(total, pos + per);
   }
-  int b = s_b;
-  long long b_first = s_before;
+  if (pos >= end) return;
+  int b = sequence_at(p, units == 1 ? pos : pos / units, &b_first);
+  b_first *= units;
 
   const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-  float4 *meta = reinterpret_cast<float4 *>(smem + C::OFF_META) + warp * C::STAGES;
+  float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE) + warp * C::STAGES * C::NS;
   float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);   // [warp][ROWS]
+  const uint32_t copy_dst = tile_at<D>(lane / C::CH, lane % C::CH);
 
   while (pos < end) {
     int ng = granules_of(p, b);
@@ -229,58 +233,51 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
     const int group = p.Hq / p.Hkv;
     const long long row_base = ((long long)b * p.Hq + (long long)h * group) * p.Nq;   // row 0 of q, o, lse
 
-    // ---- pages: lane i holds page, sk and log2 sv of step 32 k + i
-    const int steps = g1 - g0;
+    // ---- pages: lane i holds the page number of the warp's subtile 32 k + i
+    const int subs = g1 - g0;                             // subtiles of this warp
+    const int steps = (subs + C::NS - 1) / C::NS;
     const int *tab = p.table + (long long)b * p.max_pages;
-    auto token_of = [&](int s) { return ((g0 + s) * kWarps + warp) * kStep; };
-    struct Pages {
-      int pg;
-      float sk, lsv;
+    auto token_of = [&](int i) { return (g0 + i) * kGranule + warp * kSub; };
+    auto lookup = [&](int i) {
+      const int j = token_of(i);
+      return i < subs && j < len ? checked_page(tab, j >> p.page_log2, p.num_pages, p.err) : -1;
     };
-    auto lookup = [&](int s) {
-      Pages x{-1, 0.f, 0.f};
-      const int j = token_of(s);
-      if (s < steps && j < len) {
-        x.pg = checked_page(tab, j >> p.page_log2, p.num_pages, p.err);
-        if (x.pg >= 0) {
-          x.sk = p.k_scale[(long long)x.pg * p.Hkv + h];
-          x.lsv = log2f(p.v_scale[(long long)x.pg * p.Hkv + h]);
-        }
-      }
-      return x;
-    };
-    Pages cur = lookup(lane), nxt = lookup(32 + lane);
-    // Copies of step s into its stage; always one commit group a step.
-    auto issue = [&](int s) {
+    int cur = lookup(lane), nxt = subs > 32 ? lookup(32 + lane) : -1;
+    // Copies of step s into stage st; always one commit group a step.  What
+    // is no token of the sequence becomes zeros, and its page's scales too.
+    auto issue = [&](int s, int st) {
       if (s < steps) {
-        if (s && (s & 31) == 0) {
+        const int i0 = s * C::NS;
+        if (i0 && (i0 & 31) == 0) {
           cur = nxt;
-          nxt = lookup(s + 32 + lane);
+          nxt = lookup(i0 + 32 + lane);
         }
-        const int pg = __shfl_sync(0xffffffffu, cur.pg, s & 31);
-        const float sk = __shfl_sync(0xffffffffu, cur.sk, s & 31);
-        const float lsv = __shfl_sync(0xffffffffu, cur.lsv, s & 31);
-        const int j = token_of(s);
-        const int nv = pg < 0 ? 0 : min(kStep, len - j);
-        const int st = s % C::STAGES;
-        if (lane == 0) meta[st] = make_float4(sk, lsv, __int_as_float(nv), 0.f);
-        if (nv > 0) {
-          const long long at = (((long long)pg * p.Hkv + h) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
-          const uint8_t *ks = p.k_cache + at * D, *vs = p.v_cache + at * D;
-          const uint32_t dst = ring + st * C::STAGE;
-          constexpr int RPI = 32 / C::CH;   // tokens a warp-wide copy covers
+        const uint32_t stage = ring + st * C::STAGE;
 #pragma unroll
-          for (int i = 0; i < kStep / RPI; ++i) {
-            const int r = i * RPI + lane / C::CH, c = lane % C::CH;
-            const int src = r < nv ? r * D + c * 16 : 0;   // tokens behind the length: zeros
-            cp_async16(dst + tile_at<D>(r, c), ks + src, r < nv);
-            cp_async16(dst + kStep * D + tile_at<D>(r, c), vs + src, r < nv);
+        for (int n = 0; n < C::NS; ++n) {
+          const int pg = __shfl_sync(0xffffffffu, cur, (i0 + n) & 31);
+          const int j = token_of(i0 + n);
+          const int live = pg < 0 ? 0 : min(kSub, len - j) * C::CH;   // chunks
+          const long long page_h = (long long)max(pg, 0) * p.Hkv + h;
+          const long long at = ((page_h << p.page_log2) + (j & ((1 << p.page_log2) - 1))) * D + lane * 16;
+          const uint8_t *ks = p.k_cache + at, *vs = p.v_cache + at;
+          const uint32_t dst = stage + 2 * n * C::TILE;
+#pragma unroll
+          for (int i = 0; i < C::TILE / 512; ++i) {
+            const bool in = 32 * i + lane < live;
+            const int off = in ? 512 * i : 0;
+            cp_async16(dst + tile_chunk<D>(copy_dst, i), in ? ks + off : p.k_cache, in);
+            cp_async16(dst + C::TILE + tile_chunk<D>(copy_dst, i), in ? vs + off : p.v_cache, in);
           }
+          if (lane < 2)
+            cp_async4(smem_u32(scales + st * C::NS + n) + 4 * lane,
+                      (lane ? p.v_scale : p.k_scale) + page_h, pg >= 0);
         }
       }
       cp_async_commit();
     };
-    for (int s = 0; s < C::STAGES - 1; ++s) issue(s);
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) issue(s, s);
 
     // ---- q: A fragments of halves, each row times a power of two
     uint32_t qa[MT][C::CH][4];
@@ -289,24 +286,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
     int lim_min = len;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      uint2 raw[2][C::CH];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + mt * 16 + g + 8 * e;
         const bool live = r < p.R;
         const __nv_bfloat16 *src = p.q + (row_base + (live ? r : 0)) * D + 4 * t;
-        uint2 raw[C::CH];
-        float mx = 0.f;
 #pragma unroll
         for (int c = 0; c < C::CH; ++c)
-          raw[c] = live ? *reinterpret_cast<const uint2 *>(src + 16 * c) : make_uint2(0u, 0u);
+          raw[e][c] = live ? *reinterpret_cast<const uint2 *>(src + 16 * c) : make_uint2(0u, 0u);
+        lim[mt][e] = !live ? 0 : (p.causal ? max(0, len - p.Nq + r % p.Nq + 1) : len);
+        if (live) lim_min = min(lim_min, lim[mt][e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = 0.f;
 #pragma unroll
         for (int c = 0; c < C::CH; ++c) {
-          const uint32_t w[2] = {raw[c].x, raw[c].y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] << 16)));
-            mx = fmaxf(mx, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
-          }
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[e][c].x << 16)),
+                               fabsf(__uint_as_float(raw[e][c].x & 0xFFFF0000u))));
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[e][c].y << 16)),
+                               fabsf(__uint_as_float(raw[e][c].y & 0xFFFF0000u))));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -316,13 +316,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
         row_c[mt][e] = p.scale_log2 * __uint_as_float((uint32_t)(k - 13 + 127) << 23);
 #pragma unroll
         for (int c = 0; c < C::CH; ++c) {
-          qa[mt][c][e] = pack_half2(__uint_as_float(raw[c].x << 16) * up,
-                                    __uint_as_float(raw[c].x & 0xFFFF0000u) * up);
-          qa[mt][c][2 + e] = pack_half2(__uint_as_float(raw[c].y << 16) * up,
-                                        __uint_as_float(raw[c].y & 0xFFFF0000u) * up);
+          qa[mt][c][e] = pack_half2(__uint_as_float(raw[e][c].x << 16) * up,
+                                    __uint_as_float(raw[e][c].x & 0xFFFF0000u) * up);
+          qa[mt][c][2 + e] = pack_half2(__uint_as_float(raw[e][c].y << 16) * up,
+                                        __uint_as_float(raw[e][c].y & 0xFFFF0000u) * up);
         }
-        lim[mt][e] = !live ? 0 : (p.causal ? max(0, len - p.Nq + r % p.Nq + 1) : len);
-        if (live) lim_min = min(lim_min, lim[mt][e]);
       }
     }
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
@@ -342,32 +340,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       }
     }
 
+    int st = 0;   // stage of step s
+#pragma unroll 1
     for (int s = 0; s < steps; ++s) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
-      issue(s + C::STAGES - 1);
-      const int st = s % C::STAGES;
-      const float4 mt4 = meta[st];
-      const int nv = __float_as_int(mt4.z);
-      if (nv <= 0) continue;
-      const float sk = mt4.x, lsv = mt4.y;
-      const int j0 = token_of(s);
-      const uint32_t kt = ring + st * C::STAGE, vt = kt + kStep * D;
+      issue(s + C::STAGES - 1, st == 0 ? C::STAGES - 1 : st - 1);
+      const uint32_t stage = ring + st * C::STAGE;
 
-      // ---- S = q K^T: two groups of 8 tokens
-      float sc[MT][2][4];
+      // ---- S = q K^T: two groups of 8 tokens a subtile
+      float sc[MT][2 * C::NS][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2 * C::NS; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < C::CH; c += 4)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < 2 * C::NS; ++n) {
           uint32_t kb[4];
-          ldsm4(kt + tile_at<D>(8 * n + (lane & 7), c + (lane >> 3)), kb);
+          ldsm4(stage + (n >> 1) * 2 * C::TILE + tile_at<D>(8 * (n & 1) + (lane & 7), c + (lane >> 3)), kb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t b0 = e4m3x2_to_half2(kb[i]), b1 = e4m3x2_to_half2(kb[i] >> 16);
@@ -377,36 +371,53 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
         }
 
       // ---- softmax
-      const bool whole = nv == kStep && j0 + kStep <= lim_min;
+      float sk[C::NS], lsv[C::NS];
+      int j0[C::NS], nv[C::NS];
+      bool whole = true;
+#pragma unroll
+      for (int n = 0; n < C::NS; ++n) {
+        const float2 x = scales[st * C::NS + n];
+        j0[n] = token_of(s * C::NS + n);
+        // a subtile without a page has scales 0: no token of it is visible
+        nv[n] = x.y > 0.f ? min(kSub, len - j0[n]) : 0;
+        sk[n] = x.x;
+        lsv[n] = nv[n] > 0 ? __log2f(x.y) : 0.f;
+        whole = whole && nv[n] == kSub && j0[n] + kSub <= lim_min;
+      }
       bool moved = false;
-      float mx[MT][2];
+      float mxs[MT][2], mxo[MT][2];   // row maxima of s and of s + log2 sv
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float cf = row_c[mt][e] * sk;
-          const int lm = min(nv, lim[mt][e] - j0);
+          mxs[mt][e] = mxo[mt][e] = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < C::NS; ++n) {
+            const float cf = row_c[mt][e] * sk[n];
+            float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x = sc[mt][n][2 * e + i] * cf;
-              if (!whole && 8 * n + 2 * t + i >= lm) x = -INFINITY;
-              sc[mt][n][2 * e + i] = x;
+            for (int i = 0; i < 4; ++i) {
+              float x = sc[mt][2 * n + (i >> 1)][2 * e + (i & 1)] * cf;
+              if (!whole && 8 * (i >> 1) + 2 * t + (i & 1) >= min(nv[n], lim[mt][e] - j0[n])) x = -INFINITY;
+              sc[mt][2 * n + (i >> 1)][2 * e + (i & 1)] = x;
+              mx = fmaxf(mx, x);
             }
-          mx[mt][e] = fmaxf(fmaxf(sc[mt][0][2 * e], sc[mt][0][2 * e + 1]),
-                            fmaxf(sc[mt][1][2 * e], sc[mt][1][2 * e + 1]));
-          moved |= mx[mt][e] > fminf(m_s[mt][e], m_o[mt][e] - lsv) + kLag;
+            mxs[mt][e] = fmaxf(mxs[mt][e], mx);
+            mxo[mt][e] = fmaxf(mxo[mt][e], mx + lsv[n]);
+          }
+          moved |= mxs[mt][e] > m_s[mt][e] + kLag || mxo[mt][e] > m_o[mt][e] + kLag;
         }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = mx[mt][e];
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            const float ns = fmaxf(m_s[mt][e], v), no = fmaxf(m_o[mt][e], v + lsv);
+            float vs = mxs[mt][e], vo = mxo[mt][e];
+            vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
+            vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 1));
+            vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 2));
+            vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 2));
+            const float ns = fmaxf(m_s[mt][e], vs), no = fmaxf(m_o[mt][e], vo);
             // a row that has seen no key yet has l = 0 and O = 0
             const float al = ns == m_s[mt][e] ? 1.f : fast_exp2(m_s[mt][e] - ns);
             const float ao = no == m_o[mt][e] ? 1.f : fast_exp2(m_o[mt][e] - no);
@@ -420,20 +431,25 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
             }
           }
       }
-      uint32_t pa[MT][4];
+      uint32_t pa[MT][C::NS][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const bool none = m_s[mt][e] == -INFINITY;
           const float ms = none ? 0.f : m_s[mt][e];
-          const float gain = none ? 0.f : fast_exp2(m_s[mt][e] - m_o[mt][e] + lsv + kShift);
+          const float diff = none ? 0.f : m_s[mt][e] - m_o[mt][e] + kShift;
           float sum = 0.f;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = fast_exp2(sc[mt][n][2 * e] - ms), p1 = fast_exp2(sc[mt][n][2 * e + 1] - ms);
-            sum += p0 + p1;
-            pa[mt][2 * n + e] = pack_half2(p0 * gain, p1 * gain);
+          for (int n = 0; n < C::NS; ++n) {
+            const float gain = fast_exp2(diff + lsv[n]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p0 = fast_exp2(sc[mt][2 * n + i][2 * e] - ms);
+              const float p1 = fast_exp2(sc[mt][2 * n + i][2 * e + 1] - ms);
+              sum += p0 + p1;
+              pa[mt][n][2 * i + e] = pack_half2(p0 * gain, p1 * gain);
+            }
           }
           l[mt][e] += sum;
         }
@@ -441,12 +457,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       // ---- a token that some row does not see may hold a NaN code in V, and
       // 0 * NaN is NaN: such codes become 0, and the columns of the rows that
       // do see the token become NaN
-      if (j0 + nv > lim_min) {
+#pragma unroll
+      for (int n = 0; n < C::NS; ++n) {
+        if (j0[n] + nv[n] <= lim_min) continue;
 #pragma unroll 1
-        for (int w = lane; w < kStep * D / 4; w += 32) {
+        for (int w = lane; w < C::TILE / 4; w += 32) {
           const int r = w / (D / 4), col = (w - r * (D / 4)) * 4;
           uint32_t *word = reinterpret_cast<uint32_t *>(
-              smem + warp * kRingBytes + st * C::STAGE + kStep * D + tile_at<D>(r, col >> 4) + (col & 15));
+              smem + warp * kRingBytes + st * C::STAGE + (2 * n + 1) * C::TILE + tile_at<D>(r, col >> 4) +
+              (col & 15));
           const uint32_t nan4 = __vcmpeq4(*word & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
           unsigned who = __ballot_sync(0xffffffffu, nan4 != 0);
           if (nan4) *word &= ~nan4;
@@ -457,12 +476,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int n = 0; n < D / 8; ++n)
+              for (int k = 0; k < D / 8; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const int at = 16 * (n >> 1) + (n & 1) + 4 * t + 2 * (e & 1) - cc;   // column within the word
-                  if (at >= 0 && at < 4 && ((bytes >> (8 * at)) & 1u) && j0 + rr < lim[mt][e >> 1])
-                    o[mt][n][e] = __uint_as_float(0x7FC00000u);
+                  const int at = 16 * (k >> 1) + (k & 1) + 4 * t + 2 * (e & 1) - cc;   // column within the word
+                  if (at >= 0 && at < 4 && ((bytes >> (8 * at)) & 1u) && j0[n] + rr < lim[mt][e >> 1])
+                    o[mt][k][e] = __uint_as_float(0x7FC00000u);
                 }
           }
         }
@@ -472,26 +491,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       // ---- O += P V: ldmatrix.trans hands out pairs of columns of two
       // tokens; a byte swap makes them pairs of tokens of one column
 #pragma unroll
-      for (int c = 0; c < C::CH; c += 2) {
-        uint32_t vb[4];   // chunk c: tokens 0-7, 8-15; chunk c + 1: the same
-        ldsm4_trans(vt + tile_at<D>((lane & 7) + (lane & 8), c + (lane >> 4)), vb);
+      for (int n = 0; n < C::NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w0 = __byte_perm(vb[2 * i], 0, 0x3120), w1 = __byte_perm(vb[2 * i + 1], 0, 0x3120);
-          const uint32_t e0 = e4m3x2_to_half2(w0), e1 = e4m3x2_to_half2(w1);
-          const uint32_t d0 = e4m3x2_to_half2(w0 >> 16), d1 = e4m3x2_to_half2(w1 >> 16);
+        for (int c = 0; c < C::CH; c += 2) {
+          uint32_t vb[4];   // chunk c: tokens 0-7, 8-15; chunk c + 1: the same
+          ldsm4_trans(stage + (2 * n + 1) * C::TILE + tile_at<D>((lane & 7) + (lane & 8), c + (lane >> 4)), vb);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_f16(o[mt][2 * (c + i)], pa[mt], e0, e1);       // columns 16 (c + i) + 2 n
-            mma_f16(o[mt][2 * (c + i) + 1], pa[mt], d0, d1);   // and + 1
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w0 = __byte_perm(vb[2 * i], 0, 0x3120), w1 = __byte_perm(vb[2 * i + 1], 0, 0x3120);
+            const uint32_t e0 = e4m3x2_to_half2(w0), e1 = e4m3x2_to_half2(w1);
+            const uint32_t d0 = e4m3x2_to_half2(w0 >> 16), d1 = e4m3x2_to_half2(w1 >> 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_f16(o[mt][2 * (c + i)], pa[mt][n], e0, e1);       // columns 16 (c + i) + 2 k
+              mma_f16(o[mt][2 * (c + i) + 1], pa[mt][n], d0, d1);   // and + 1
+            }
           }
         }
-      }
+      st = st + 1 == C::STAGES ? 0 : st + 1;
     }
     cp_async_wait<0>();
 
     // ---- the four warps' results joined: each row's log-sum-exp first
-    float fac[MT][2];
+    const int rows = min(C::ROWS, p.R - r0);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -503,37 +525,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
         if (t == 0) stat[warp * C::ROWS + mt * 16 + g + 8 * e] = v == 0.f ? -INFINITY : m_s[mt][e] + log2f(v);
       }
     __syncthreads();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = mt * 16 + g + 8 * e;
-        float top = -INFINITY, sum = 0.f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
-        for (int w = 0; w < kWarps; ++w)
-          sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : exp2f(stat[w * C::ROWS + r] - top);
-        // O / l_warp * 2^{L_warp - L} = O 2^{M - shift - m} / l * ...
-        fac[mt][e] = l[mt][e] == 0.f ? 0.f
-                                     : exp2f(m_o[mt][e] - kShift - m_s[mt][e]) / l[mt][e] *
-                                           (exp2f(stat[warp * C::ROWS + r] - top) / sum);
-      }
     // o of columns 16 c + 4 t .. + 3 lies in two accumulators
     float *mine = reinterpret_cast<float *>(smem + warp * kRingBytes);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        const int r = mt * 16 + g + 8 * e;
+        if (r >= rows) continue;
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < C::CH; ++c) {
-          const float f = fac[mt][e];
-          *reinterpret_cast<float4 *>(mine + (mt * 16 + g + 8 * e) * D + 16 * c + 4 * t) =
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
+        // O / l_warp * 2^{L_warp - L}, O being in units of 2^{M - shift - m}
+        const float f = l[mt][e] == 0.f ? 0.f
+                                        : fast_exp2(m_o[mt][e] - kShift - m_s[mt][e]) / l[mt][e] *
+                                              (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c)
+          *reinterpret_cast<float4 *>(mine + r * D + 16 * c + 4 * t) =
               make_float4(o[mt][2 * c][2 * e] * f, o[mt][2 * c + 1][2 * e] * f,
                           o[mt][2 * c][2 * e + 1] * f, o[mt][2 * c + 1][2 * e + 1] * f);
-        }
+      }
     __syncthreads();
     const bool final = g0 == 0 && g1 == ng;
     const long long part = ((long long)blockIdx.x * 2 + (g0 == 0 ? 1 : 0)) * p.prows;
-    const int rows = min(C::ROWS, p.R - r0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
       const int r = i / (D / 4), c4 = i - r * (D / 4);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -553,7 +571,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       float top = -INFINITY, sum = 0.f;
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
       for (int w = 0; w < kWarps; ++w)
-        sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : exp2f(stat[w * C::ROWS + r] - top);
+        sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
       const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);
       if (final) p.lse[row_base + r0 + r] = L2 * 0.69314718055994531f;
       else p.l_part[part + r] = L2;
@@ -578,17 +596,18 @@ __device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
 
 // Joins the pieces of the units that several CTAs covered, one CTA per query
 // row; rows of sequences without tokens become O = 0, L = -inf.
+constexpr int kMergeWarps = 8;
+
 template <int D, int MT>
-__global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const RowParams p) {
   using C = RowCfg<D, MT>;
-  __shared__ long long s_red[4];
-  __shared__ float s_o[4][D], s_w[kMaxCtas];
-  const long long row = blockIdx.x;
-  const int b = (int)(row / ((long long)p.Hq * p.Nq));
-  const int hr = (int)(row - (long long)b * p.Hq * p.Nq);   // row within the sequence
-  const int h = hr / p.R, r = hr - h * p.R, tile = r / C::ROWS;
+  __shared__ float s_o[kMergeWarps][D], s_w[kMaxCtas];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x;
+  const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
+  const int h = hr / p.R, r = hr - h * p.R, tile = r / C::ROWS, rr = r - tile * C::ROWS;
   const int ng = granules_of(p, b);
-  __nv_bfloat16 *dst = p.o + row * D;
+  __nv_bfloat16 *dst = p.o + (long long)row * D;
   if (ng == 0) {
     wait_for_primary();
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
@@ -598,47 +617,51 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p)
     }
     return;
   }
-  long long total, before;
-  line_of(p, b, s_red, &total, &before);
-  const long long per = (total + p.ctas - 1) / p.ctas;
-  const long long first = before + ((long long)h * p.tiles + tile) * ng;
-  const int c0 = (int)(first / per), c1 = (int)((first + ng - 1) / per);
+  long long total, first;
+  line_of(p, b, &total, &first);
+  const int units = p.Hkv * p.tiles;
+  const long long per = (total * units + p.ctas - 1) / p.ctas;
+  first = first * units + ((long long)h * p.tiles + tile) * ng;
+  const int c0 = (int)(first / per), n = (int)((first + ng - 1) / per) - c0 + 1;
   // every CTA waits, so that what follows in the stream finds o and lse whole
   wait_for_primary();
-  if (c0 == c1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = r - tile * C::ROWS;
-  const int n = c1 - c0 + 1;
+  if (n == 1) return;
+  // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
   auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
-  // every warp forms the same maximum and sum; each keeps a quarter of the weights
+  constexpr int PER = D / 32, AHEAD = 8;
+  const float *src = p.o_part + lane * PER;
+  // warp w adds pieces w, w + 8, ...: the first loads go out before the weights are known
+  float v[AHEAD][PER];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (warp + kMergeWarps * k < n) load_floats<PER>(src + at(warp + kMergeWarps * k) * D, v[k]);
   float top = -INFINITY, sum = 0.f;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   for (int i = lane; i < n; i += 32) {
     const float x = p.l_part[at(i)];
-    const float w = x == -INFINITY ? 0.f : exp2f(x - top);
+    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
     sum += w;
-    if ((i & 3) == warp) s_w[i] = w;
+    if (i % kMergeWarps == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   __syncwarp();
-  // warp w adds pieces w, w + 4, ...: eight loads in flight
-  constexpr int PER = D / 32;
   float acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  const float *src = p.o_part + lane * PER;
 #pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += 32) {
-    float v[8][PER];
+  for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
+    if (i0 != warp) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + 4 * k < n) load_floats<PER>(src + at(i0 + 4 * k) * D, v[k]);
+      for (int k = 0; k < AHEAD; ++k)
+        if (i0 + kMergeWarps * k < n) load_floats<PER>(src + at(i0 + kMergeWarps * k) * D, v[k]);
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + 4 * k < n) {
-        const float w = s_w[i0 + 4 * k];
+    for (int k = 0; k < AHEAD; ++k)
+      if (i0 + kMergeWarps * k < n) {
+        const float w = s_w[i0 + kMergeWarps * k];
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
       }
@@ -648,10 +671,13 @@ __global__ void __launch_bounds__(128) fwd_cache_merge_kernel(const RowParams p)
   for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e] * inv;
   __syncthreads();
   if (threadIdx.x < D / 2) {
-    const int c = 2 * threadIdx.x;
-    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] =
-        pack_bf16x2((s_o[0][c] + s_o[1][c]) + (s_o[2][c] + s_o[3][c]),
-                    (s_o[0][c + 1] + s_o[1][c + 1]) + (s_o[2][c + 1] + s_o[3][c + 1]));
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      x += s_o[w][2 * threadIdx.x];
+      y += s_o[w][2 * threadIdx.x + 1];
+    }
+    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
   }
   if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
@@ -709,7 +735,7 @@ int run_rows(const CacheArgs &a, const RowPlan &x) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq * a.Nq), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = a.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
