@@ -29,11 +29,9 @@
 // It has a reference M of its own, the running maximum of s + log2 sv: terms
 // down to 2^-26 of the largest keep 11 bits whatever the pages' scales, and
 // smaller ones err by at most 2^-37 of the largest weight.
-#include <math.h>
-
 #include <type_traits>
 
-#include "cache.cuh"
+#include "fwd_cache.cuh"
 
 namespace fa {
 namespace {
@@ -43,7 +41,7 @@ constexpr int kSub = 16;                        // tokens of a subtile (one page
 constexpr int kGranule = kWarps * kSub;
 constexpr int kStage = 8 * 1024, kStages = 3;   // a warp's ring
 constexpr int kRing = kStage * kStages;
-constexpr int kMaxCtas = 2 * 148;               // two per SM
+using RowLine = Line<16, kGranule, false>;
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
 constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 
@@ -152,131 +150,15 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Programmatic dependent launch: the next kernel of the stream may start; a
-// dependent kernel waits here until the one before it has ended.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_primary() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-struct RowParams {
-  const __nv_bfloat16 *q;
-  const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;
-  const int *table, *lens;
-  __nv_bfloat16 *o;
-  float *lse;
-  float *o_part, *l_part;   // [ctas][2][prows][D], [ctas][2][prows] (base 2)
-  int B, Hq, Hkv, Nq, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
-  int page_log2, num_pages, max_pages;
-  int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
-  float scale_log2;
-  unsigned *err;
-};
-
-__device__ __forceinline__ int granules_of(const RowParams &p, int b) {
-  const int n = p.lens[b];
-  return (min(max(n, 0), p.max_pages << p.page_log2) + kGranule - 1) / kGranule;
-}
-
-__device__ __forceinline__ int warp_sum(int v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
-// The line of granules: sequences in order, each with Hkv * tiles units of
-// granules_of(b) (fewer than 2^31 in all: the launcher checks).  Granules of
-// all sequences, and of those before sequence b, of one unit each; every warp
-// forms them for itself.
-__device__ __forceinline__ void line_of(const RowParams &p, int b, int *total, int *before) {
-  int all = 0, pre = 0;
-  for (int i = threadIdx.x & 31; i < p.B; i += 32) {
-    const int n = granules_of(p, i);
-    all += n;
-    if (i < b) pre += n;
-  }
-  *total = warp_sum(all);
-  *before = b > 0 ? warp_sum(pre) : 0;
-}
-
-// The sequence that holds granule `pos` of the line cut to one unit a
-// sequence (pos < the total), and the granules before it.
-__device__ __forceinline__ int sequence_at(const RowParams &p, int pos, int *before) {
-  const int lane = threadIdx.x & 31;
-  int base = 0;
-  for (int i0 = 0;; i0 += 32) {
-    const int n = i0 + lane < p.B ? granules_of(p, i0 + lane) : 0;
-    int inc = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    inc += base;
-    const unsigned past = __ballot_sync(0xffffffffu, pos < inc);
-    if (past || i0 + 32 >= p.B) {
-      const int at = past ? __ffs(past) - 1 : 31;
-      *before = __shfl_sync(0xffffffffu, inc - n, at);
-      return min(i0 + at, p.B - 1);
-    }
-    base = __shfl_sync(0xffffffffu, inc, 31);
-  }
-}
-
-// A CTA's run of the line, piece by piece.
-struct Run {
-  int pos, end;        // granules left: [pos, end)
-  int b, b_first;      // the sequence of the current piece, the line's granules before it
-  // the current piece: granules [g0, g1) of ng of the unit (b, h, row tile
-  // from r0 on), tokens [.., stop) of the sequence's len
-  int h, r0, g0, g1, ng, len, stop;
-
-  __device__ __forceinline__ bool start(const RowParams &p) {
-    int total, unused;
-    line_of(p, 0, &total, &unused);
-    const int units = p.Hkv * p.tiles;
-    total *= units;
-    const int per = (total + p.ctas - 1) / p.ctas;
-    pos = per * (int)blockIdx.x;      // at most total + per
-    end = min(total, pos + per);
-    if (pos >= end) return false;
-    b = sequence_at(p, pos / units, &b_first);
-    b_first *= units;
-    return true;
-  }
-  __device__ __forceinline__ bool next(const RowParams &p, int rows) {
-    if (pos >= end) return false;
-    const int units = p.Hkv * p.tiles;
-    ng = granules_of(p, b);
-    while (pos - b_first >= ng * units) {   // on to the next sequence with tokens
-      b_first += ng * units;
-      ++b;
-      ng = granules_of(p, b);
-    }
-    const int u = (pos - b_first) / ng;
-    g0 = pos - b_first - u * ng;
-    g1 = min(ng, g0 + (end - pos));
-    pos += g1 - g0;
-    h = u / p.tiles;
-    r0 = (u - h * p.tiles) * rows;
-    len = min(max(p.lens[b], 0), p.max_pages << p.page_log2);
-    stop = min(len, g1 * kGranule);
-    return true;
-  }
-};
-
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const FwdCacheParams p) {
   using C = RowCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   launch_dependents();   // the merge kernel's CTAs may take their places
-  Run run;
-  if (!run.start(p) || !run.next(p, C::ROWS)) return;
+  Run<RowLine> run;
+  if (!run.start(p) || !run.next(p)) return;
 
   const uint32_t sbase = smem_u32(smem), ring = sbase + warp * kRing;
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE) + warp * kStages * C::NS;
@@ -600,9 +482,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
 
     // ---- on to the next piece: its first copies go out before the merge
     const long long row0 = ((long long)run.b * p.Hkv + run.h) * p.R + run.r0;
-    const int part = run.g0 == 0 && run.g1 == run.ng
-                         ? -1   // the piece is the whole unit
-                         : ((int)blockIdx.x * 2 + (run.g0 == 0 ? 1 : 0)) * p.prows;
+    const int part = run.part(p);
     // each row's log-sum-exp in this warp
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -613,7 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
       if (t == 0) stat[warp * C::ROWS + g + 8 * e] = v == 0.f ? -INFINITY : m_s[e] + log2f(v);
     }
     __syncthreads();   // every warp is done with q and its ring
-    const bool more = run.next(p, C::ROWS);
+    const bool more = run.next(p);
     if (more) begin(st);
 
     // ---- the four warps' results joined
@@ -674,173 +554,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Ro
   }
 }
 
-template <int PER>
-__device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
-  if constexpr (PER == 2) {
-    const float2 x = *reinterpret_cast<const float2 *>(src);
-    v[0] = x.x; v[1] = x.y;
-  } else {
-#pragma unroll
-    for (int e = 0; e < PER; e += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(src + e);
-      v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
-    }
-  }
-}
-
-// Joins the pieces of the units that several CTAs covered, one CTA per query
-// row; rows of sequences without tokens become O = 0, L = -inf.
-constexpr int kMergeWarps = 8;
-
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const RowParams p) {
+int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   using C = RowCfg<D>;
-  __shared__ float s_o[kMergeWarps][D], s_w[kMaxCtas];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x;
-  const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
-  const int h = hr / p.R, r = hr - h * p.R, tile = r / C::ROWS, rr = r - tile * C::ROWS;
-  const int ng = granules_of(p, b);
-  __nv_bfloat16 *dst = p.o + (long long)row * D;
-  if (ng == 0) {
-    wait_for_primary();
-    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) {
-      p.lse[row] = -INFINITY;
-      if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
-    }
-    return;
-  }
-  int total, first;
-  line_of(p, b, &total, &first);
-  const int units = p.Hkv * p.tiles;
-  const int per = (total * units + p.ctas - 1) / p.ctas;
-  first = first * units + (h * p.tiles + tile) * ng;
-  const int c0 = first / per, n = (first + ng - 1) / per - c0 + 1;
-  // every CTA waits, so that what follows in the stream finds o and lse whole
-  wait_for_primary();
-  if (n == 1) return;
-  // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
-  auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
-  constexpr int PER = D / 32, AHEAD = 8;
-  const float *src = p.o_part + lane * PER;
-  // warp w adds pieces w, w + 8, ...: the first loads go out before the weights are known
-  float v[AHEAD][PER];
-#pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-    if (warp + kMergeWarps * k < n) load_floats<PER>(src + at(warp + kMergeWarps * k) * D, v[k]);
-  float top = -INFINITY, sum = 0.f;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  for (int i = lane; i < n; i += 32) {
-    const float x = p.l_part[at(i)];
-    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-    sum += w;
-    if (i % kMergeWarps == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  __syncwarp();
-  float acc[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-#pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
-    if (i0 != warp) {
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (i0 + kMergeWarps * k < n) load_floats<PER>(src + at(i0 + kMergeWarps * k) * D, v[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (i0 + kMergeWarps * k < n) {
-        const float w = s_w[i0 + kMergeWarps * k];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-      }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e] * inv;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      x += s_o[w][2 * threadIdx.x];
-      y += s_o[w][2 * threadIdx.x + 1];
-    }
-    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
-  }
-  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-}
-
-// What the host knows of the work: rows, tiles, CTAs (two per SM, fewer when
-// the block table has room for fewer granules).
-struct RowPlan {
-  double R, most;   // most: granules when every sequence fills its table
-  int prows, ctas;
-  long long tiles;
-};
-RowPlan plan_of(const CacheArgs &a) {
-  RowPlan x;
-  x.R = (double)(a.Hq / a.Hkv) * a.Nq;
-  x.prows = x.R < 16 ? (int)x.R : 16;
-  x.tiles = (long long)((x.R + 15) / 16);
-  x.most = (double)a.B * a.Hkv * x.tiles * (((long long)a.max_pages * a.page + kGranule - 1) / kGranule);
-  x.ctas = x.most < kMaxCtas ? (int)x.most : kMaxCtas;
-  return x;
-}
-
-template <int D>
-int run_rows(const CacheArgs &a, const RowPlan &x) {
-  using C = RowCfg<D>;
-  RowParams p;
-  p.q = (const __nv_bfloat16 *)a.q;
-  p.k_cache = a.k_cache; p.v_cache = a.v_cache;
-  p.k_scale = a.k_scale; p.v_scale = a.v_scale;
-  p.table = a.table; p.lens = a.lens;
-  p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
-  p.o_part = (float *)a.ws;
-  p.l_part = p.o_part + (size_t)x.ctas * 2 * x.prows * D;
-  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq;
-  p.R = (int)x.R;
-  p.tiles = (int)x.tiles;
-  p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;
-  p.num_pages = a.num_pages; p.max_pages = a.max_pages;
-  p.causal = a.causal; p.ctas = x.ctas; p.prows = x.prows;
-  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-  p.err = a.err;
+  const FwdCacheParams p = fwd_cache_params(a, x);
   auto kern = fwd_cache_rows_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return 5;
   kern<<<x.ctas, kWarps * 32, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
-  // The merge kernel is launched while the main one runs: its CTAs find their
-  // pieces, then wait for the main kernel's end.
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq * a.Nq), 1, 1);
-  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
-  cfg.stream = a.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D>, p) != cudaSuccess) return 5;
-  return cudaGetLastError() == cudaSuccess ? 0 : 5;
+  return launch_fwd_cache_merge<D, RowLine>(p, a.stream);
 }
+
+FwdCachePlan rows_plan(const CacheArgs &a) { return fwd_cache_plan(a, RowLine::ROWS, kGranule, 2 * 148); }
 
 }  // namespace
 
-size_t fwd_cache_ws_bytes(const CacheArgs &a) {
-  const RowPlan x = plan_of(a);
-  return (size_t)x.ctas * 2 * x.prows * (a.d + 1) * 4;
-}
+size_t fwd_cache_ws_bytes(const CacheArgs &a) { return fwd_cache_plan_bytes(rows_plan(a), a.d); }
 
 int launch_fwd_cache(const CacheArgs &a) {
-  const RowPlan x = plan_of(a);
+  const FwdCachePlan x = rows_plan(a);
   // the line's granules are counted in int32
   if (x.R > 2147483647.0 || x.most > 2.0e9) return 2;
   switch (a.d) {

@@ -6,9 +6,13 @@
 //
 // Memory-bound: every element is read once and written once, 16 bytes at a
 // time.  A thread owns V pairs of one position (two vectors of V columns) and
-// takes their cos and sin once for up to kMaxHeads heads of q and k, so the
-// float64 angles and the sine cost little beside the traffic; with few
-// positions (decoding) the heads are spread over more threads instead.
+// takes their cos and sin once for several heads of q and k.
+//
+// Angles: f_p / 2 pi mod 1, formed in float64, becomes a 64-bit fraction of a
+// turn (once a block, in shared memory); times the position, modulo 2^64, it is
+// the fraction of the turn at t, whose upper 32 bits go to float32.  So the
+// reduction costs an integer product, and a position of millions keeps its
+// angle: 2^-32 of a turn beside what float64 rounds in f_p / 2 pi, times t.
 #include "common.cuh"
 #include "launch.h"
 
@@ -61,39 +65,39 @@ __device__ __forceinline__ Raw pack(const float (&x)[V]) {
 
 // Thread (position, group c): c < pair_groups turns V pairs, whose vectors
 // start at columns u and w (half layout: V c and V c + rot / 2; interleaved: 2
-// V c and 2 V c + V); the others copy the vector from column `rot` on.
-// blockIdx.y: heads [y * per, y * per + per) of q's and then k's.
+// V c and 2 V c + V); the groups behind them copy two vectors (the last perhaps
+// one).  Blocks are (groups, positions); blockIdx.y: heads [y * per, y * per +
+// per) of q's and then k's.
 template <class T, int V, bool INTER>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, int groups, int pair_groups, int per) {
+__global__ void __launch_bounds__(64) rope_kernel(const RopeArgs a, int pair_groups, int per) {
   using Raw = typename Vec<T, V>::Raw;
-  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long bn = idx / groups;
-  if (bn >= (long long)a.B * a.N) return;
-  const int c = (int)(idx - bn * groups);
-  const int b = (int)(bn / a.N), n = (int)(bn - (long long)b * a.N);
-  const int h0 = blockIdx.y * per, h1 = min(h0 + per, a.Hq + a.Hkv);
-  // element (head h, position n, column 0) of q or k
-  auto row = [&](int h) {
-    return h < a.Hq ? (((long long)b * a.Hq + h) * a.N + n) * a.d
-                    : (((long long)b * a.Hkv + h - a.Hq) * a.N + n) * a.d;
-  };
-  auto in = [&](int h) { return (const T *)(h < a.Hq ? a.q : a.k) + row(h); };
-  auto out = [&](int h) { return (T *)(h < a.Hq ? a.q_out : a.k_out) + row(h); };
-  constexpr int AHEAD = 4;   // heads in flight
-  if (c >= pair_groups) {
-    const int u = a.rot + (c - pair_groups) * V;
-    for (int h = h0; h < h1; h += AHEAD) {
-      Raw x[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-        if (h + i < h1) x[i] = *reinterpret_cast<const Raw *>(in(h + i) + u);
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-        if (h + i < h1) *reinterpret_cast<Raw *>(out(h + i) + u) = x[i];
-    }
-    return;
+  __shared__ unsigned long long s_turn[128];
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.rot / 2; i += blockDim.x * blockDim.y) {
+    double r = a.freqs[i] * 0.15915494309189533577;
+    r -= floor(r);   // whole turns a token do not matter
+    s_turn[i] = __double2ull_rn(r * 18446744073709551616.0);   // 2^64 (1 saturates: 2^-64 off)
   }
-  const int u = INTER ? 2 * V * c : V * c, w = INTER ? u + V : u + a.rot / 2;
+  const int c = threadIdx.x;
+  const unsigned bn = blockIdx.x * blockDim.y + threadIdx.y;   // B * N is below 2^31
+  const bool live = bn < (unsigned)a.B * (unsigned)a.N;
+  const unsigned b = live ? bn / (unsigned)a.N : 0, n = live ? bn - b * a.N : 0;
+  const int h0 = blockIdx.y * per, h1 = live ? min(h0 + per, a.Hq + a.Hkv) : h0;
+  // this position's row of head 0 of q and, Hq heads back, of k
+  const long long head = (long long)a.N * a.d;
+  const long long q0 = (long long)b * a.Hq * head + (long long)n * a.d;
+  const long long k0 = ((long long)b * a.Hkv - a.Hq) * head + (long long)n * a.d;
+  auto in = [&](int h) { return (const T *)(h < a.Hq ? a.q : a.k) + ((h < a.Hq ? q0 : k0) + h * head); };
+  auto out = [&](int h) { return (T *)(h < a.Hq ? a.q_out : a.k_out) + ((h < a.Hq ? q0 : k0) + h * head); };
+  const bool turns = c < pair_groups;
+  int u, w;
+  if (turns) {
+    u = INTER ? 2 * V * c : V * c;
+    w = INTER ? u + V : u + a.rot / 2;
+  } else {
+    u = a.rot + 2 * V * (c - pair_groups);
+    w = u + V < a.d ? u + V : u;   // an odd vector at the end: copied twice
+  }
+  constexpr int AHEAD = 2;   // heads in flight
   Raw x[AHEAD], y[AHEAD];
   // the first heads' loads are under way while the angles are formed
 #pragma unroll
@@ -103,16 +107,17 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, int groups,
       y[i] = *reinterpret_cast<const Raw *>(in(h0 + i) + w);
     }
   float cs[V], sn[V];
-  const double t = (double)a.positions[a.pos_per_batch ? bn : n];
+  const int t = !live ? 0 : a.positions[a.pos_per_batch ? bn : n];
+  __syncthreads();
+  if (turns) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    // turns of the circle in float64, reduced to [-1/2, 1/2] before float32:
-    // the angle of any int32 position keeps 2^-25 half turns
-    double r = t * (a.freqs[V * c + i] * 0.15915494309189533577);
-    r -= rint(r);
-    sincospif((float)(2.0 * r), &sn[i], &cs[i]);
-    cs[i] *= a.mscale;
-    sn[i] *= a.backward ? -a.mscale : a.mscale;
+    for (int i = 0; i < V; ++i) {
+      const unsigned long long turn = s_turn[V * c + i] * (unsigned long long)(long long)t;
+      // half turns in [-1, 1)
+      sincospif((float)(int)(turn >> 32) * 4.656612873077392578125e-10f, &sn[i], &cs[i]);
+      cs[i] *= a.mscale;
+      sn[i] *= a.backward ? -a.mscale : a.mscale;
+    }
   }
   for (int h = h0; h < h1; h += AHEAD) {
     if (h != h0) {
@@ -126,45 +131,50 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a, int groups,
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (h + i >= h1) continue;
-      float p[V], q[V], ru[V], rw[V];
-      unpack<T, V>(x[i], p);
-      unpack<T, V>(y[i], q);
+      if (turns) {
+        float p[V], q[V], ru[V], rw[V];
+        unpack<T, V>(x[i], p);
+        unpack<T, V>(y[i], q);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if constexpr (INTER) {   // pair e: elements 2 e, 2 e + 1 of the two vectors
-          const float p0 = 2 * e < V ? p[(2 * e) % V] : q[(2 * e) % V];
-          const float p1 = 2 * e < V ? p[(2 * e + 1) % V] : q[(2 * e + 1) % V];
-          const float r0 = p0 * cs[e] - p1 * sn[e], r1 = p1 * cs[e] + p0 * sn[e];
-          if (2 * e < V) { ru[(2 * e) % V] = r0; ru[(2 * e + 1) % V] = r1; }
-          else { rw[(2 * e) % V] = r0; rw[(2 * e + 1) % V] = r1; }
-        } else {
-          ru[e] = p[e] * cs[e] - q[e] * sn[e];
-          rw[e] = q[e] * cs[e] + p[e] * sn[e];
+        for (int e = 0; e < V; ++e) {
+          if constexpr (INTER) {   // pair e: elements 2 e, 2 e + 1 of the two vectors
+            const float p0 = 2 * e < V ? p[(2 * e) % V] : q[(2 * e) % V];
+            const float p1 = 2 * e < V ? p[(2 * e + 1) % V] : q[(2 * e + 1) % V];
+            const float r0 = p0 * cs[e] - p1 * sn[e], r1 = p1 * cs[e] + p0 * sn[e];
+            if (2 * e < V) { ru[(2 * e) % V] = r0; ru[(2 * e + 1) % V] = r1; }
+            else { rw[(2 * e) % V] = r0; rw[(2 * e + 1) % V] = r1; }
+          } else {
+            ru[e] = p[e] * cs[e] - q[e] * sn[e];
+            rw[e] = q[e] * cs[e] + p[e] * sn[e];
+          }
         }
+        x[i] = pack<T, V, Raw>(ru);
+        y[i] = pack<T, V, Raw>(rw);
       }
-      *reinterpret_cast<Raw *>(out(h + i) + u) = pack<T, V, Raw>(ru);
-      *reinterpret_cast<Raw *>(out(h + i) + w) = pack<T, V, Raw>(rw);
+      *reinterpret_cast<Raw *>(out(h + i) + u) = x[i];
+      *reinterpret_cast<Raw *>(out(h + i) + w) = y[i];
     }
   }
 }
 
 constexpr int kMaxHeads = 32;        // heads that share a thread's cos and sin, at most
-constexpr long long kThreads = 148LL * 1024;   // threads that fill the GPU
+constexpr long long kThreads = 148LL * 2048;   // threads that fill the GPU
 
 template <class T, int V, bool INTER>
 int run(const RopeArgs &a) {
   const int pair_groups = a.rot / (2 * V);
   // in place, the columns that do not turn are there already
   const bool in_place = a.q == a.q_out && a.k == a.k_out;
-  const int groups = pair_groups + (in_place ? 0 : (a.d - a.rot) / V);
+  const int groups = pair_groups + (in_place ? 0 : ((a.d - a.rot) / V + 1) / 2);
   const long long one = (long long)a.B * a.N * groups;   // threads of one head
+  // positions of a block: 64 threads (B4 H16 N4096 d128 measured 45.2 us with
+  // 64, 45.8 with 128, 47.8 with 256)
+  const int deep = groups < 64 ? 64 / groups : 1;
   const int heads = a.Hq + a.Hkv;
   int per = heads < kMaxHeads ? heads : kMaxHeads;
   while (per > 1 && one * ((heads + per - 1) / per) < kThreads) per = (per + 1) / 2;
-  const long long blocks = (one + 255) / 256;
-  if (blocks > 2147483647LL) return 2;
-  const dim3 grid((unsigned)blocks, (unsigned)((heads + per - 1) / per));
-  rope_kernel<T, V, INTER><<<grid, 256, 0, a.stream>>>(a, groups, pair_groups, per);
+  const dim3 grid((unsigned)(((long long)a.B * a.N + deep - 1) / deep), (unsigned)((heads + per - 1) / per));
+  rope_kernel<T, V, INTER><<<grid, dim3(groups, deep), 0, a.stream>>>(a, pair_groups, per);
   return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 

@@ -1,0 +1,332 @@
+// fwd_cache.cuh -- what the two kernels of attention over the paged cache share:
+// parameters, the division of the work among CTAs, the merge of partial results.
+#pragma once
+
+#include <math.h>
+
+#include "cache.cuh"
+
+namespace fa {
+
+// Programmatic dependent launch: the next kernel of the stream may start; a
+// dependent kernel waits here until the one before it has ended.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+constexpr int kMaxCtas = 2 * 148;   // CTAs of a launch, at most
+
+struct FwdCacheParams {
+  const __nv_bfloat16 *q;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int *table, *lens;
+  __nv_bfloat16 *o;
+  float *lse;
+  float *o_part, *l_part;   // [ctas][2][prows][D], [ctas][2][prows] (base 2)
+  int B, Hq, Hkv, Nq, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
+  int page_log2, num_pages, max_pages;
+  int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
+  float scale_log2;
+  unsigned *err;
+};
+
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// The work: a unit is (sequence, key/value head, tile of ROWS query rows), its
+// tokens in granules of GRANULE.  The granules of all units stand in one line
+// (sequences in order, each its heads, each its tiles; fewer than 2^31: the
+// launcher checks), which is cut into p.ctas even runs.
+//
+// QMAJOR: row r of a head is query r / g of its group's head r % g, so a tile
+// holds consecutive queries and, causal, sees no further than its last one;
+// else row r is query r % Nq of head r / Nq, the order of memory, and every tile
+// of a sequence has the same granules.
+template <int ROWS_, int GRANULE_, bool QMAJOR_>
+struct Line {
+  static constexpr int ROWS = ROWS_, GRANULE = GRANULE_;
+  static constexpr bool QMAJOR = QMAJOR_;
+
+  static __device__ __forceinline__ int len(const FwdCacheParams &p, int b) {
+    return min(max(p.lens[b], 0), p.max_pages << p.page_log2);
+  }
+  // tokens that some row of the tile sees, as granules
+  static __device__ __forceinline__ int granules(const FwdCacheParams &p, int len, int tile) {
+    int seen = len;
+    if (QMAJOR && p.causal) {
+      const int last = (min(p.R, (tile + 1) * ROWS) - 1) / (p.Hq / p.Hkv);
+      seen = max(0, len - p.Nq + last + 1);
+    }
+    return (seen + GRANULE - 1) / GRANULE;
+  }
+  // granules of one head: all its tiles
+  static __device__ __forceinline__ int head(const FwdCacheParams &p, int len) {
+    if constexpr (!QMAJOR) return granules(p, len, 0) * p.tiles;
+    int sum = 0;
+    for (int t = 0; t < p.tiles; ++t) sum += granules(p, len, t);
+    return sum;
+  }
+  // The granules of one head of all sequences, and of those before sequence
+  // b; every warp forms them for itself.
+  static __device__ __forceinline__ void sums(const FwdCacheParams &p, int b, int *total, int *before) {
+    int all = 0, pre = 0;
+    for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+      const int n = head(p, len(p, i));
+      all += n;
+      if (i < b) pre += n;
+    }
+    *total = warp_sum(all);
+    *before = b > 0 ? warp_sum(pre) : 0;
+  }
+  // The sequence that holds granule `pos` of the line cut to one head a
+  // sequence (pos < the total), and the granules before it.
+  static __device__ __forceinline__ int sequence_at(const FwdCacheParams &p, int pos, int *before) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int i0 = 0;; i0 += 32) {
+      const int n = i0 + lane < p.B ? head(p, len(p, i0 + lane)) : 0;
+      int inc = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      inc += base;
+      const unsigned past = __ballot_sync(0xffffffffu, pos < inc);
+      if (past || i0 + 32 >= p.B) {
+        const int at = past ? __ffs(past) - 1 : 31;
+        *before = __shfl_sync(0xffffffffu, inc - n, at);
+        return min(i0 + at, p.B - 1);
+      }
+      base = __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+};
+
+// A CTA's run of the line, piece by piece.
+template <class L>
+struct Run {
+  int pos, end;        // granules left: [pos, end)
+  int b, b_first;      // the sequence of the current piece, the line's granules before it
+  // the current piece: granules [g0, g1) of ng of the unit (b, h, tile from
+  // row r0 on), tokens [.., stop) of the sequence's len
+  int h, r0, g0, g1, ng, len, stop;
+
+  __device__ __forceinline__ bool start(const FwdCacheParams &p) {
+    int total, unused;
+    L::sums(p, 0, &total, &unused);
+    total *= p.Hkv;
+    const int per = (total + p.ctas - 1) / p.ctas;
+    pos = per * (int)blockIdx.x;      // at most total + per
+    end = min(total, pos + per);
+    if (pos >= end) return false;
+    b = L::sequence_at(p, pos / p.Hkv, &b_first);
+    b_first *= p.Hkv;
+    return true;
+  }
+  __device__ __forceinline__ bool next(const FwdCacheParams &p) {
+    if (pos >= end) return false;
+    len = L::len(p, b);
+    int n = L::head(p, len);
+    while (pos - b_first >= n * p.Hkv) {   // on to the next sequence with tokens
+      b_first += n * p.Hkv;
+      ++b;
+      len = L::len(p, b);
+      n = L::head(p, len);
+    }
+    h = (pos - b_first) / n;
+    int rest = pos - b_first - h * n, tile;
+    if constexpr (L::QMAJOR) {
+      for (tile = 0; rest >= (ng = L::granules(p, len, tile)); ++tile) rest -= ng;
+    } else {
+      ng = L::granules(p, len, 0);
+      tile = rest / ng;
+      rest -= tile * ng;
+    }
+    g0 = rest;
+    g1 = min(ng, g0 + (end - pos));
+    pos += g1 - g0;
+    r0 = tile * L::ROWS;
+    stop = min(len, g1 * L::GRANULE);
+    return true;
+  }
+  // first row of the piece's partial, -1 where the piece is the whole unit: a
+  // run has at most one piece that starts inside its unit (slot 0) and one that
+  // starts a unit and does not end it (slot 1)
+  __device__ __forceinline__ int part(const FwdCacheParams &p) const {
+    return g0 == 0 && g1 == ng ? -1 : ((int)blockIdx.x * 2 + (g0 == 0 ? 1 : 0)) * p.prows;
+  }
+};
+
+template <int PER>
+__device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
+  if constexpr (PER == 2) {
+    const float2 x = *reinterpret_cast<const float2 *>(src);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; e += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(src + e);
+      v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
+    }
+  }
+}
+
+// Joins the pieces of the units that several CTAs covered, one CTA per query
+// row; rows of tiles that see no token become O = 0, L = -inf.
+constexpr int kMergeWarps = 8;
+
+template <int D, class L>
+__global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const FwdCacheParams p) {
+  __shared__ float s_o[kMergeWarps][D], s_w[kMaxCtas];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x;
+  const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
+  const int h = hr / p.R;
+  int r = hr - h * p.R;   // row of the head, in the order of memory
+  if constexpr (L::QMAJOR) r = r % p.Nq * (p.Hq / p.Hkv) + r / p.Nq;
+  const int tile = r / L::ROWS, rr = r - tile * L::ROWS;
+  const int len = L::len(p, b), ng = L::granules(p, len, tile);
+  __nv_bfloat16 *dst = p.o + (long long)row * D;
+  if (ng == 0) {
+    wait_for_primary();
+    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) {
+      p.lse[row] = -INFINITY;
+      if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
+    }
+    return;
+  }
+  int total, first;
+  L::sums(p, b, &total, &first);
+  const int per = (total * p.Hkv + p.ctas - 1) / p.ctas;
+  first = first * p.Hkv + h * L::head(p, len);
+  if constexpr (L::QMAJOR)
+    for (int t = 0; t < tile; ++t) first += L::granules(p, len, t);
+  else
+    first += tile * ng;
+  const int c0 = first / per, n = (first + ng - 1) / per - c0 + 1;
+  // every CTA waits, so that what follows in the stream finds o and lse whole
+  wait_for_primary();
+  if (n == 1) return;
+  // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
+  auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
+  constexpr int PER = D / 32, AHEAD = 8;
+  const float *src = p.o_part + lane * PER;
+  // warp w adds pieces w, w + 8, ...: the first loads go out before the weights are known
+  float v[AHEAD][PER];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (warp + kMergeWarps * k < n) load_floats<PER>(src + at(warp + kMergeWarps * k) * D, v[k]);
+  float top = -INFINITY, sum = 0.f;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  for (int i = lane; i < n; i += 32) {
+    const float x = p.l_part[at(i)];
+    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+    sum += w;
+    if (i % kMergeWarps == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  __syncwarp();
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
+    if (i0 != warp) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (i0 + kMergeWarps * k < n) load_floats<PER>(src + at(i0 + kMergeWarps * k) * D, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (i0 + kMergeWarps * k < n) {
+        const float w = s_w[i0 + kMergeWarps * k];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+      }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e] * inv;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      x += s_o[w][2 * threadIdx.x];
+      y += s_o[w][2 * threadIdx.x + 1];
+    }
+    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
+  }
+  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+// Launches the merge while the main kernel runs: its CTAs find their pieces,
+// then wait for the main kernel's end.
+template <int D, class L>
+int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hq * p.Nq), 1, 1);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L>, p) != cudaSuccess) return 5;
+  return cudaGetLastError() == cudaSuccess ? 0 : 5;
+}
+
+// What the host knows of the work of tiles of `rows` rows and granules of
+// `granule` tokens: CTAs (fewer than `most_ctas` when the block table has room
+// for fewer granules), rows of a partial.
+struct FwdCachePlan {
+  double R, most;   // most: granules when every sequence fills its table
+  long long tiles;
+  int prows, ctas;
+};
+inline FwdCachePlan fwd_cache_plan(const CacheArgs &a, int rows, int granule, int most_ctas) {
+  FwdCachePlan x;
+  x.R = (double)(a.Hq / a.Hkv) * a.Nq;
+  x.prows = x.R < rows ? (int)x.R : rows;
+  x.tiles = (long long)((x.R + rows - 1) / rows);
+  x.most = (double)a.B * a.Hkv * x.tiles * (((long long)a.max_pages * a.page + granule - 1) / granule);
+  x.ctas = x.most < most_ctas ? (int)x.most : most_ctas;
+  return x;
+}
+inline size_t fwd_cache_plan_bytes(const FwdCachePlan &x, int d) {
+  return (size_t)x.ctas * 2 * x.prows * (d + 1) * 4;
+}
+inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x) {
+  FwdCacheParams p;
+  p.q = (const __nv_bfloat16 *)a.q;
+  p.k_cache = a.k_cache; p.v_cache = a.v_cache;
+  p.k_scale = a.k_scale; p.v_scale = a.v_scale;
+  p.table = a.table; p.lens = a.lens;
+  p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
+  p.o_part = (float *)a.ws;
+  p.l_part = p.o_part + (size_t)x.ctas * 2 * x.prows * a.d;
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq;
+  p.R = (int)x.R;
+  p.tiles = (int)x.tiles;
+  p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;
+  p.num_pages = a.num_pages; p.max_pages = a.max_pages;
+  p.causal = a.causal; p.ctas = x.ctas; p.prows = x.prows;
+  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  p.err = a.err;
+  return p;
+}
+
+}  // namespace fa
