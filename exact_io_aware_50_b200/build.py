@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_capi.cu", "fa_simt.cu", "fa_fwd_sm100.cu", "fa_bwd_sm100.cu", "fa_noalloc.cu",
-           "fa_capi_cache.cu", "fa_rope.cu", "fa_cache.cu", "fa_fwd_cache.cu"]
+           "fa_capi_cache.cu", "fa_rope.cu", "fa_cache.cu", "fa_fwd_cache.cu",
+           "fa_fwd_cache_sm100.cu"]
 HEADERS = ["common.cuh", "cta_pair.cuh", "cache.cuh", "fwd_cache.cuh", "launch.h"]
 
 

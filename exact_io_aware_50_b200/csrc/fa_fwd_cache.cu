@@ -566,16 +566,27 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   return launch_fwd_cache_merge<D, RowLine>(p, a.stream);
 }
 
-FwdCachePlan rows_plan(const CacheArgs &a) { return fwd_cache_plan(a, RowLine::ROWS, kGranule, 2 * 148); }
+// One tile of 16 rows: the kernel of this file; more rows read the cache once
+// for 128 of them on tcgen05.
+bool few_rows(const CacheArgs &a) { return (double)(a.Hq / a.Hkv) * a.Nq <= RowLine::ROWS; }
+
+FwdCachePlan plan_of(const CacheArgs &a) {
+  return few_rows(a) ? fwd_cache_plan(a, RowLine::ROWS, kGranule, kMaxCtas) : fwd_cache_tile_plan(a);
+}
 
 }  // namespace
 
-size_t fwd_cache_ws_bytes(const CacheArgs &a) { return fwd_cache_plan_bytes(rows_plan(a), a.d); }
+size_t fwd_cache_ws_bytes(const CacheArgs &a) { return fwd_cache_plan_bytes(plan_of(a), a.d); }
 
 int launch_fwd_cache(const CacheArgs &a) {
-  const FwdCachePlan x = rows_plan(a);
+  const FwdCachePlan x = plan_of(a);
   // the line's granules are counted in int32
   if (x.R > 2147483647.0 || x.most > 2.0e9) return 2;
+  if (!few_rows(a)) {
+    // cache rows (of d codes) are counted in uint32 there
+    if ((double)a.num_pages * a.Hkv * a.page >= 4294967295.0) return 2;
+    return launch_fwd_cache_tiles(a, x);
+  }
   switch (a.d) {
     case 64: return run_rows<64>(a, x);
     case 128: return run_rows<128>(a, x);

@@ -1,0 +1,626 @@
+// fa_fwd_cache_sm100.cu -- attention over the paged E4M3 cache for many query
+// rows (chunks of a prompt, drafted tokens of grouped heads): tiles of 128 rows
+// on tcgen05, TMEM accumulators.
+//
+// The mathematics are those of fa_fwd_cache.cu, with the same two references
+// (m for the sum of 2^{s - m}, M for the weights 2^{s - m} sv) and the same
+// roundings: q and the weights as halves, the codes exactly as halves.
+//
+// A CTA (one per SM, 12 warps) takes NT tiles of 128 rows of one key/value
+// head, row r being query r / g of the group's head r % g, and blocks of 128
+// tokens of its run of the line:
+//   warps 0 .. 4 NT - 1  softmax and epilogue, a thread per row (TMEM lane)
+//   the others but one   converters: they read q rows and the pages' codes into
+//                        registers a block ahead, and write halves into
+//                        128-byte-swizzled shared memory when the block before
+//                        has left it; tokens that do not exist become zeros
+//   warp 11              issues the MMAs (lane 0)
+// S_t = Q_t K^T lands in TMEM; the softmax thread reads its row, which frees S
+// for the next block's product, and writes the weights to shared memory; O_t +=
+// P_t V accumulates in TMEM.  All MMAs are kind::f16 with halves: M 128, N 128
+// (N d for O).  E4M3 operands would halve the product's cost but hold a weight
+// to 4 bits (8 in two parts, which cost as much as halves), down to 2^-18 of
+// the largest only; converting 128 tokens costs about 90 instructions a warp,
+// beside 4000 cycles that a block takes in the softmax.
+#include "fwd_cache.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int kMmaWarp = 11;
+constexpr int kThreads = 384;
+constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
+constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
+constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
+
+template <int D_, int NT_>
+struct TileCfg {
+  static constexpr int D = D_, NT = NT_;
+  using L = Line<NT * BM, BN, true>;
+  static constexpr int SOFT = 4 * NT;                 // softmax warps
+  static constexpr int CONV = kMmaWarp - SOFT;        // converter warps
+  static constexpr int CT = CONV * 32;
+  static constexpr int CHUNK = BN * 128;              // 128 rows of 64 halves
+  static constexpr int DCH = D / 64;
+  static constexpr int TILE = CHUNK * DCH;            // Q, K or V as halves
+  static constexpr int P_TILE = CHUNK * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_P = OFF_Q + NT * TILE;
+  static constexpr int OFF_K = OFF_P + NT * P_TILE;
+  static constexpr int OFF_V = OFF_K + TILE;
+  static constexpr int OFF_ROWC = OFF_V + TILE;       // [NT * 128] float: scale of a row's scores
+  static constexpr int OFF_SCALE = OFF_ROWC + NT * BM * 4;   // [4][8] (sk, log2 sv) of a block's 16-token groups
+  static constexpr int OFF_NAN = OFF_SCALE + 4 * 8 * 8;      // [2][D] first NaN token of a column
+  static constexpr int OFF_ANY = OFF_NAN + 2 * D * 4;        // [2] whether there is one
+  static constexpr int OFF_PIECE = OFF_ANY + 8;              // [2] Piece
+  static constexpr int OFF_BAR = OFF_PIECE + 2 * 32;
+  static constexpr int NBAR = 11 + 6 * NT;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;        // TMEM base, abort flag
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int TM_S = 0, TM_O = NT * BN;
+  static_assert(NT * (BN + D) <= 512, "TMEM budget");
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// The other roles' copy of the converters' piece; no blocks: the run is over.
+struct Piece {
+  int b, h, r0, blocks, token, len, part, unused;
+};
+static_assert(sizeof(Piece) == 32, "Piece");
+
+// D[tmem] (+)= A B with halves: the format fields 0.
+constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// 16 E4M3 codes -> 16 halves, in the 16-byte units at `at` and `at ^ 16`.
+__device__ __forceinline__ void store_halves(uint32_t at, const uint4 &codes) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[2 * i] = e4m3x2_to_half2(w[i] & 0xFFFFu);
+    h[2 * i + 1] = e4m3x2_to_half2(w[i] >> 16);
+  }
+  st_shared_v4(at, h[0], h[1], h[2], h[3]);
+  st_shared_v4(at ^ 16, h[4], h[5], h[6], h[7]);
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCacheParams p) {
+  constexpr int D = C::D, NT = C::NT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrConfig);
+    return;
+  }
+  launch_dependents();   // the merge kernel's CTAs may take their places
+  auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
+  constexpr int B_UFULL = 0, B_UEMPTY = 2, B_QFULL = 4, B_QEMPTY = 5, B_KFULL = 6, B_KEMPTY = 7,
+                B_VFULL = 8, B_VEMPTY = 9, B_DRAIN = 10, B_SFULL = 11, B_SEMPTY = 11 + NT,
+                B_PFULL = 11 + 2 * NT, B_PEMPTY = 11 + 3 * NT, B_OFULL = 11 + 4 * NT,
+                B_OEMPTY = 11 + 5 * NT;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  float *row_c = reinterpret_cast<float *>(smem + C::OFF_ROWC);
+  float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE);
+  // Two lists of NaN codes, for pieces in turn.  A piece's converters clear the
+  // next piece's list before they hand over their last V.
+  int *nan_at = reinterpret_cast<int *>(smem + C::OFF_NAN), *nan_any = reinterpret_cast<int *>(smem + C::OFF_ANY);
+  Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_PIECE);
+  const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_UFULL + i), 1);
+      mbar_init(bar(B_UEMPTY + i), NT * BM + 1);   // softmax threads, the MMA issuer
+    }
+    mbar_init(bar(B_QFULL), C::CT);
+    mbar_init(bar(B_QEMPTY), 1);
+    mbar_init(bar(B_KFULL), C::CT);
+    mbar_init(bar(B_KEMPTY), 1);
+    mbar_init(bar(B_VFULL), C::CT);
+    mbar_init(bar(B_VEMPTY), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(bar(B_SFULL + t), 1);
+      mbar_init(bar(B_SEMPTY + t), BM);
+      mbar_init(bar(B_PFULL + t), BM);
+      mbar_init(bar(B_PEMPTY + t), 1);
+      mbar_init(bar(B_OFULL + t), 1);
+      mbar_init(bar(B_OEMPTY + t), BM);
+    }
+    *abort_flag = 0;
+    nan_any[0] = nan_any[1] = 0;
+    fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_at[i] = 0x7FFFFFFF;
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{p.err, abort_flag, kWaitLimitNs};
+  const int group = p.Hq / p.Hkv;
+
+  // Blocks of the run are counted by g, pieces by u: barrier phases.
+  if (warp >= C::SOFT && warp < kMmaWarp) {
+    // ---------------------------------------------------------- converters
+    const int ct = threadIdx.x - C::SOFT * 32;    // 0 .. CT - 1
+    const bool leader = ct == 0;
+    // Four lanes take 64 columns of a token, a warp eight tokens at a time: "row"
+    // i * CT / 4 + ct / 4 of the DCH * 128 rows of 64 halves that a tile has.
+    // Its place mod 8, and so the swizzle, is the thread's own; eight lanes store
+    // to eight bank groups.
+    constexpr int RPI = C::CT / 4, ROWS = BN * C::DCH;
+    constexpr int NL = (ROWS + RPI - 1) / RPI;    // chunks of 16 codes of a thread
+    static_assert(RPI % 8 == 0, "the swizzle is the thread's own");
+    const int ct4 = ct >> 2;
+    const uint32_t my_dst = sbase + ct4 * 128 + ((((ct & 3) * 2) ^ (ct4 & 7)) << 4);
+    const uint32_t my_src = (ct & 3) * 16;
+    bool ok = true;
+    int g = 0, u = 0;
+    Run<typename C::L> run;
+    bool more = run.start(p);
+    for (; ok; ++u) {
+      if (more) more = run.next(p);
+      const int n = more ? run.g1 - run.g0 : 0;
+      if (leader) {
+        ok = bounded_wait(bar(B_UEMPTY + (u & 1)), ((u >> 1) & 1) ^ 1, wc);
+        if (ok) {
+          Piece x;
+          x.b = run.b; x.h = run.h; x.r0 = run.r0; x.blocks = n;
+          x.token = run.g0 * BN; x.len = run.len;
+          x.part = more ? run.part(p) : -1;
+          x.unused = 0;
+          pieces[u & 1] = x;
+          mbar_arrive(bar(B_UFULL + (u & 1)));
+          if (more) (void)checked_len(p.lens, run.b, p.max_pages, 1 << p.page_log2, p.err);
+        }
+      }
+      if (warp == C::SOFT) ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!more || !ok) break;
+      const int *tab = p.table + (long long)run.b * p.max_pages;
+      // of a block's 16-token group `lane` (lanes 0 .. 7): the cache row of its
+      // first token (rows of d codes), kNone: no page
+      constexpr uint32_t kNone = 0xFFFFFFFFu;
+      auto lookup = [&](int j) {
+        const int tok = (run.g0 + j) * BN + lane * 16;
+        if (lane >= 8 || j >= n || tok >= run.len) return kNone;
+        const int pg = checked_page(tab, tok >> p.page_log2, p.num_pages, p.err);
+        return pg < 0 ? kNone
+                      : (((uint32_t)pg * p.Hkv + run.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+      };
+      // this thread's chunks of K or V of block j, whose groups lie at `rows`
+      auto load = [&](const uint8_t *cache, int j, uint32_t rows, uint4 (&x)[NL]) {
+        const int left = run.len - (run.g0 + j) * BN;   // tokens there are
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int row = i * RPI + ct4, r = row & (BN - 1);
+          const uint32_t at = __shfl_sync(0xffffffffu, rows, r >> 4);
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row < ROWS && at != kNone && r < left)
+            x[i] = *reinterpret_cast<const uint4 *>(cache + (size_t)(at + (r & 15)) * D + (row / BN) * 64 + my_src);
+        }
+      };
+      auto store = [&](int tile, const uint4 (&x)[NL]) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+          if (i * RPI + ct4 < ROWS) store_halves(my_dst + tile + i * RPI * 128, x[i]);
+      };
+      // (sk, log2 sv) of a group; without a page (1, -inf): nothing visible
+      auto scale_of = [&](uint32_t row) {
+        if (row == kNone) return make_float2(1.f, -INFINITY);
+        const uint32_t i = row >> p.page_log2;
+        return make_float2(p.k_scale[i], log2f(p.v_scale[i]));
+      };
+      // ---- the first blocks' codes are on their way while q is converted
+      uint32_t pg0 = lookup(0), pg1 = lookup(1), pg2 = lookup(2);   // of blocks j, j + 1, j + 2
+      uint4 kr[NL], vr[NL];
+      load(p.k_cache, 0, pg0, kr);
+      load(p.v_cache, 0, pg0, vr);
+      float2 sc = scale_of(pg0);
+
+      // ---- q: 16 or 32 lanes a row (8 at d = 64), each row times a power of
+      // two that brings its largest entry to [2^13, 2^14)
+      ok = warp_wait_all(bar(B_QEMPTY), (u & 1) ^ 1, wc);
+      // the softmax has read row_c by the time it has read its last S
+      for (int t = 0; t < NT && ok && u > 0; ++t) ok = warp_wait_all(bar(B_SEMPTY + t), (g - 1) & 1, wc);
+      if (!ok) break;
+      int lim_min = run.len;   // tokens that every row of the piece sees
+      {
+        constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes of a row, rows of a warp at a time
+        constexpr int AHEAD = 4;
+        const int sub = lane / LPR, col = lane % LPR;
+        for (int r = (ct >> 5) * RPW; r < NT * BM; r += C::CONV * RPW * AHEAD) {
+          uint4 raw[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const int row = r + k * C::CONV * RPW + sub, rr = run.r0 + row;
+            raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < NT * BM && rr < p.R) {
+              const int i = rr / group, hq = run.h * group + rr - i * group;
+              raw[k] = *reinterpret_cast<const uint4 *>(
+                  p.q + (((long long)run.b * p.Hq + hq) * p.Nq + i) * D + col * 8);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const int row = r + k * C::CONV * RPW + sub;
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1)
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
+            const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+            if (row < NT * BM) {
+              if (col == 0)
+                row_c[row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                h[i] = pack_half2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+              st_shared_v4(sbase + C::OFF_Q + (row >> 7) * C::TILE + (col >> 3) * C::CHUNK + (row & 127) * 128 +
+                               (((col & 7) ^ (row & 7)) << 4),
+                           h[0], h[1], h[2], h[3]);
+            }
+          }
+        }
+        if (p.causal) lim_min = max(0, min(run.len, run.len - p.Nq + run.r0 / group + 1));
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(B_QFULL));
+
+      for (int j = 0; j <= n && ok; ++j) {
+        // K runs a block ahead of V
+        if (j < n) {
+          ok = warp_wait_all(bar(B_KEMPTY), ((g + j) & 1) ^ 1, wc);
+          if (!ok) break;
+          if (ct < 8) scales[((g + j) & 3) * 8 + ct] = sc;
+          store(C::OFF_K, kr);
+          fence_proxy_async_smem();
+          mbar_arrive(bar(B_KFULL));
+          if (j + 1 < n) {
+            load(p.k_cache, j + 1, pg1, kr);
+            sc = scale_of(pg1);
+          }
+        }
+        if (j > 0) {   // V of block j - 1
+          const int jv = j - 1;
+          ok = warp_wait_all(bar(B_VEMPTY), ((g + jv) & 1) ^ 1, wc);
+          if (!ok) break;
+          if (j == n) {
+            // the epilogue of the piece before has read its list: clear it for
+            // the next piece, whose V waits for this one's
+            for (int t = 0; t < NT && ok && u > 0; ++t) ok = warp_wait_all(bar(B_OEMPTY + t), (u - 1) & 1, wc);
+            if (!ok) break;
+            for (int i = ct; i < D; i += C::CT) nan_at[((u + 1) & 1) * D + i] = 0x7FFFFFFF;
+            if (leader) nan_any[(u + 1) & 1] = 0;
+          }
+          store(C::OFF_V, vr);
+          // A token that some row does not see may hold a NaN code, and 0 * NaN
+          // is NaN: such codes become 0, and the epilogue makes their columns of
+          // the rows that see the first of them NaN.
+          if ((run.g0 + jv + 1) * BN > lim_min) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+              any |= (__vcmpeq4(vr[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(vr[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                      __vcmpeq4(vr[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(vr[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0;
+            if (any) {
+#pragma unroll 1
+              for (int row = ct4; row < ROWS; row += RPI) {
+                uint8_t *at = smem + C::OFF_V + (my_dst - sbase) + (row - ct4) * 128;
+#pragma unroll 1
+                for (int e = 0; e < 16; ++e) {
+                  unsigned short *h = reinterpret_cast<unsigned short *>(
+                      e < 8 ? at : smem + ((uint32_t)(at - smem) ^ 16u)) + (e & 7);
+                  if ((*h & 0x7FFFu) <= 0x7C00u) continue;
+                  *h = 0;
+                  atomicMin(nan_at + (u & 1) * D + row / BN * 64 + my_src + e, (run.g0 + jv) * BN + (row & (BN - 1)));
+                  nan_any[u & 1] = 1;
+                }
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(B_VFULL));
+          if (j < n) load(p.v_cache, j, pg0, vr);
+        }
+        pg0 = pg1;
+        pg1 = pg2;
+        pg2 = lookup(j + 3);
+      }
+      g += n;
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t IDESC_S = idesc_f16(BM, BN, 0), IDESC_PV = idesc_f16(BM, D, 1);
+    const uint64_t dq0 = sw128_desc(sbase + C::OFF_Q, 16, 1024), dk0 = sw128_desc(sbase + C::OFF_K, 16, 1024);
+    const uint64_t dv0 = sw128_desc(sbase + C::OFF_V, C::CHUNK, 1024), dp0 = sw128_desc(sbase + C::OFF_P, 16, 1024);
+    auto issue_s = [&](int t) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
+        mma_ss(tmem + C::TM_S + t * BN, desc_add(dq0, t * C::TILE + off), desc_add(dk0, off), IDESC_S, k > 0);
+      }
+    };
+    auto issue_pv = [&](int t, bool first) {
+#pragma unroll
+      for (int k = 0; k < BN / 16; ++k)
+        mma_ss(tmem + C::TM_O + t * D, desc_add(dp0, t * C::P_TILE + (k >> 2) * C::CHUNK + (k & 3) * 32),
+               desc_add(dv0, k * 16 * 128), IDESC_PV, !first || k > 0);
+    };
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0;
+      for (int u = 0; ok; ++u) {
+        ok = bounded_wait(bar(B_UFULL + (u & 1)), (u >> 1) & 1, wc);
+        if (!ok) break;
+        const int n = pieces[u & 1].blocks;
+        if (n == 0) break;
+        ok = bounded_wait(bar(B_QFULL), u & 1, wc) && bounded_wait(bar(B_KFULL), g & 1, wc);
+        // S of block 0 reuses columns that the softmax read in the piece before
+        for (int t = 0; t < NT && ok; ++t) {
+          if (g > 0) ok = bounded_wait(bar(B_SEMPTY + t), (g - 1) & 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(t);
+          mma_commit(bar(B_SFULL + t));
+        }
+        if (!ok) break;
+        mma_commit(bar(B_KEMPTY));
+        if (n == 1) mma_commit(bar(B_QEMPTY));
+        for (int j = 0; j < n && ok; ++j) {
+          const int gj = g + j;
+          if (j + 1 < n) {
+            ok = bounded_wait(bar(B_KFULL), (gj + 1) & 1, wc);
+            for (int t = 0; t < NT && ok; ++t) {
+              ok = bounded_wait(bar(B_SEMPTY + t), gj & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t);
+              mma_commit(bar(B_SFULL + t));
+            }
+            if (!ok) break;
+            mma_commit(bar(B_KEMPTY));
+            if (j + 2 == n) mma_commit(bar(B_QEMPTY));
+          }
+          ok = bounded_wait(bar(B_VFULL), gj & 1, wc);
+          for (int t = 0; t < NT && ok; ++t) {
+            ok = bounded_wait(bar(B_PFULL + t), gj & 1, wc);
+            if (ok && j == 0 && u > 0) ok = bounded_wait(bar(B_OEMPTY + t), (u - 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, j == 0);
+            mma_commit(bar(B_PEMPTY + t));
+            if (j + 1 == n) mma_commit(bar(B_OFULL + t));
+          }
+          if (ok) mma_commit(bar(B_VEMPTY));
+        }
+        g += n;
+        mbar_arrive(bar(B_UEMPTY + (u & 1)));
+      }
+      if (!ok) {
+        mma_commit(bar(B_DRAIN));   // every MMA issued so far must end before TMEM is freed
+        (void)drain_wait(bar(B_DRAIN), 0, p.err, kWaitLimitNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------- softmax, epilogue
+    const int t = warp >> 2, r = threadIdx.x & 127;   // tile, row = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + C::TM_S + t * BN, to = tmem + lane_off + C::TM_O + t * D;
+    const uint32_t prow = sbase + C::OFF_P + t * C::P_TILE + r * 128;
+    bool ok = true;
+    int g = 0;
+    for (int u = 0; ok; ++u) {
+      ok = warp_wait_all(bar(B_UFULL + (u & 1)), (u >> 1) & 1, wc);
+      if (!ok) break;
+      const Piece x = pieces[u & 1];
+      if (x.blocks == 0) break;
+      const int rr = x.r0 + t * BM + r;              // row of the head
+      const bool live = rr < p.R;
+      const int i = (live ? rr : 0) / group, hq = x.h * group + (live ? rr : 0) - i * group;
+      // tokens [0, lim) visible; the warp's least, for whole blocks
+      const int lim = !live ? x.len : (p.causal ? max(0, min(x.len, x.len - p.Nq + i + 1)) : x.len);
+      const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+      float m_s = -INFINITY, m_o = -INFINITY, l = 0.f, rc = 0.f;
+      for (int j = 0; j < x.blocks; ++j) {
+        ok = warp_wait_all(bar(B_SFULL + t), (g + j) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        if (j == 0) rc = row_c[t * BM + r];
+        uint32_t sr[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c)
+          tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(B_SEMPTY + t));   // the next block's S may take the columns
+        float *s = reinterpret_cast<float *>(sr);
+        const float2 *scs = scales + ((g + j) & 3) * 8;
+        const int col0 = x.token + j * BN;
+        // what the row does not see, or has no page: -inf
+        bool whole = col0 + BN <= lim_warp;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) whole = whole && scs[q].y != -INFINITY;
+        if (!whole) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int seen = scs[q].y == -INFINITY ? 0 : lim - col0 - 16 * q;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[16 * q + e] = e < seen ? s[16 * q + e] : -INFINITY;
+          }
+        }
+        // row maxima of s (base 2) and of s + log2 sv, by the pages' groups
+        float mxs = -INFINITY, mxo = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float2 kv = scs[q];
+          float mx = s[16 * q];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[16 * q + e]);
+          mx *= fmaxf(rc * kv.x, kTiny);
+          mxs = fmaxf(mxs, mx);
+          mxo = fmaxf(mxo, mx + kv.y);
+        }
+        const bool moved = mxs > m_s + kLag || mxo > m_o + kLag;
+        float al = 1.f, ao = 1.f;
+        const bool rescale = __any_sync(0xffffffffu, moved);
+        if (rescale) {
+          const float ns = fmaxf(m_s, mxs), no = fmaxf(m_o, mxo);
+          // a row that has seen no key yet has l = 0 and O = 0 (or nothing, block 0)
+          al = ns == m_s ? 1.f : fast_exp2(m_s - ns);
+          ao = no == m_o ? 1.f : fast_exp2(m_o - no);
+          m_s = ns;
+          m_o = no;
+        }
+        const bool none = m_s == -INFINITY;
+        const float ms = none ? 0.f : m_s, diff = none ? 0.f : m_s - m_o + kShift;
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float2 kv = scs[q];
+          const float cf = fmaxf(rc * kv.x, kTiny);
+          const float gain = fast_exp2(diff + kv.y);
+          uint32_t pk[8];
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float p0 = fast_exp2(fmaf(s[16 * q + 2 * e], cf, -ms));
+            const float p1 = fast_exp2(fmaf(s[16 * q + 2 * e + 1], cf, -ms));
+            part[e & 3] += p0 + p1;
+            pk[e] = pack_half2(p0 * gain, p1 * gain);
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          if (q == 0 && g + j > 0) {   // P V of the block before is done with P
+            ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
+            tc_fence_after();
+            if (!ok) break;
+          }
+          // 16 columns = 32 bytes: two 16-byte units of the row
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int unit = 2 * q + k;
+            st_shared_v4(prow + (unit >> 3) * C::CHUNK + (((unit & 7) ^ (r & 7)) << 4), pk[4 * k], pk[4 * k + 1],
+                         pk[4 * k + 2], pk[4 * k + 3]);
+          }
+        }
+        l = l * al + sum;
+        if (!ok) break;
+        fence_proxy_async_smem();
+        if (rescale && j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(to + c * 32, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * ao);
+            tmem_st32(to + c * 32, ov);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL + t));
+      }
+      if (ok) ok = warp_wait_all(bar(B_OFULL + t), u & 1, wc);
+      if (!ok) break;
+      // ------------------------------------------------------------ epilogue
+      tc_fence_after();
+      const bool seen = !(l == 0.f);
+      const float f = seen ? fast_exp2(m_o - kShift - m_s) / l : 0.f;
+      const bool nans = nan_any[u & 1] != 0;
+      const long long row = ((long long)x.b * p.Hq + hq) * p.Nq + i;
+      const long long prt = x.part < 0 ? 0 : (long long)(x.part + t * BM + r);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(to + c * 32, ov);
+        tmem_wait_ld();
+        float *o = reinterpret_cast<float *>(ov);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = seen ? o[e] * f : 0.f;
+        if (nans) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (nan_at[(u & 1) * D + c * 32 + e] < lim) o[e] = __uint_as_float(0x7FC00000u);
+        }
+        if (!live) continue;
+        if (x.part < 0) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(p.o_part + prt * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (live) {
+        const float l2 = seen ? m_s + log2f(l) : -INFINITY;
+        if (x.part < 0) p.lse[row] = l2 * 0.69314718055994531f;
+        else p.l_part[prt] = l2;
+      }
+      tc_fence_before();
+      mbar_arrive(bar(B_OEMPTY + t));
+      mbar_arrive(bar(B_UEMPTY + (u & 1)));
+      g += x.blocks;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <class C>
+int run_tiles(const CacheArgs &a, const FwdCachePlan &x) {
+  const FwdCacheParams p = fwd_cache_params(a, x);
+  auto kern = fwd_cache_tile_kernel<C>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return 5;
+  kern<<<x.ctas, kThreads, C::SMEM, a.stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return 5;
+  return launch_fwd_cache_merge<C::D, typename C::L>(p, a.stream);
+}
+
+// Two tiles where more than one is filled and TMEM holds two (d <= 128).
+bool two_tiles(const CacheArgs &a) { return a.d <= 128 && (double)(a.Hq / a.Hkv) * a.Nq > BM; }
+
+}  // namespace
+
+FwdCachePlan fwd_cache_tile_plan(const CacheArgs &a) {
+  return fwd_cache_plan(a, two_tiles(a) ? 2 * BM : BM, BN, 148);
+}
+
+int launch_fwd_cache_tiles(const CacheArgs &a, const FwdCachePlan &x) {
+  switch (a.d) {
+    case 64: return two_tiles(a) ? run_tiles<TileCfg<64, 2>>(a, x) : run_tiles<TileCfg<64, 1>>(a, x);
+    case 128: return two_tiles(a) ? run_tiles<TileCfg<128, 2>>(a, x) : run_tiles<TileCfg<128, 1>>(a, x);
+    case 256: return run_tiles<TileCfg<256, 1>>(a, x);
+    default: return 2;
+  }
+}
+
+}  // namespace fa

@@ -179,61 +179,59 @@ __device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
   }
 }
 
-// Joins the pieces of the units that several CTAs covered, one CTA per query
-// row; rows of tiles that see no token become O = 0, L = -inf.
+// Joins the pieces of the units that several CTAs covered: W warps of a
+// CTA of kMergeWarps take one query row.  W is kMergeWarps where rows are few
+// and pieces many, 1 where there are rows enough.  Rows of tiles that see no
+// token become O = 0, L = -inf.
 constexpr int kMergeWarps = 8;
 
-template <int D, class L>
+template <int D, class L, int W>
 __global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const FwdCacheParams p) {
-  __shared__ float s_o[kMergeWarps][D], s_w[kMaxCtas];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x;
-  const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
+  __shared__ float s_o[W > 1 ? kMergeWarps : 1][D], s_w[kMaxCtas];
+  const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
+  const int row = W > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const bool exists = row < p.B * p.Hq * p.Nq;
+  const int b = exists ? row / (p.Hq * p.Nq) : 0, hr = exists ? row - b * p.Hq * p.Nq : 0;   // row within the sequence
   const int h = hr / p.R;
   int r = hr - h * p.R;   // row of the head, in the order of memory
   if constexpr (L::QMAJOR) r = r % p.Nq * (p.Hq / p.Hkv) + r / p.Nq;
   const int tile = r / L::ROWS, rr = r - tile * L::ROWS;
   const int len = L::len(p, b), ng = L::granules(p, len, tile);
-  __nv_bfloat16 *dst = p.o + (long long)row * D;
-  if (ng == 0) {
-    wait_for_primary();
-    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) {
-      p.lse[row] = -INFINITY;
-      if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
-    }
-    return;
-  }
   int total, first;
   L::sums(p, b, &total, &first);
-  const int per = (total * p.Hkv + p.ctas - 1) / p.ctas;
+  const int per = max((total * p.Hkv + p.ctas - 1) / p.ctas, 1);
   first = first * p.Hkv + h * L::head(p, len);
   if constexpr (L::QMAJOR)
     for (int t = 0; t < tile; ++t) first += L::granules(p, len, t);
   else
     first += tile * ng;
-  const int c0 = first / per, n = (first + ng - 1) / per - c0 + 1;
+  const int c0 = first / per, n = ng == 0 ? 0 : (first + ng - 1) / per - c0 + 1;
   // every CTA waits, so that what follows in the stream finds o and lse whole
   wait_for_primary();
-  if (n == 1) return;
+  if (n == 1 || !exists) return;
   // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
   auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
   constexpr int PER = D / 32, AHEAD = 8;
   const float *src = p.o_part + lane * PER;
-  // warp w adds pieces w, w + 8, ...: the first loads go out before the weights are known
+  // warp w adds pieces w, w + W, ...: the first loads go out before the weights are known
   float v[AHEAD][PER];
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k)
-    if (warp + kMergeWarps * k < n) load_floats<PER>(src + at(warp + kMergeWarps * k) * D, v[k]);
+    if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
   float top = -INFINITY, sum = 0.f;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float own = 0.f;   // lane i: the weight of piece i (W == 1: the first 32)
   for (int i = lane; i < n; i += 32) {
     const float x = p.l_part[at(i)];
     const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
     sum += w;
-    if (i % kMergeWarps == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
+    if (W > 1) {
+      if (i % W == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
+    } else if (i < 32) {
+      own = w;
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -242,50 +240,76 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += AHEAD * kMergeWarps) {
+  for (int i0 = warp; i0 < n; i0 += AHEAD * W) {
     if (i0 != warp) {
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k)
-        if (i0 + kMergeWarps * k < n) load_floats<PER>(src + at(i0 + kMergeWarps * k) * D, v[k]);
+        if (i0 + W * k < n) load_floats<PER>(src + at(i0 + W * k) * D, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
-      if (i0 + kMergeWarps * k < n) {
-        const float w = s_w[i0 + kMergeWarps * k];
+      if (i0 + W * k < n) {
+        const int i = i0 + W * k;
+        float w;
+        if (W > 1) {
+          w = s_w[i];
+        } else {
+          w = __shfl_sync(0xffffffffu, own, i & 31);
+          if (i >= 32) {   // more pieces than lanes: the weight again
+            const float x = p.l_part[at(i)];
+            w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
       }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e] * inv;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float x = 0.f, y = 0.f;
+  for (int e = 0; e < PER; ++e) acc[e] *= inv;
+  __nv_bfloat16 *dst = p.o + (long long)row * D;
+  if constexpr (W > 1) {
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      x += s_o[w][2 * threadIdx.x];
-      y += s_o[w][2 * threadIdx.x + 1];
+    for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        x += s_o[w][2 * threadIdx.x];
+        y += s_o[w][2 * threadIdx.x + 1];
+      }
+      reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
     }
-    reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+      reinterpret_cast<uint32_t *>(dst)[(lane * PER + e) / 2] = pack_bf16x2(acc[e], acc[e + 1]);
   }
-  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  if (lane == 0 && warp == 0) {
+    p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
+  }
 }
 
 // Launches the merge while the main kernel runs: its CTAs find their pieces,
 // then wait for the main kernel's end.
 template <int D, class L>
 int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
+  const long long rows = (long long)p.B * p.Hq * p.Nq;
+  const bool many = rows > 1184;   // a warp a row fills the GPU's first 148 CTAs of eight
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hq * p.Nq), 1, 1);
+  cfg.gridDim = dim3((unsigned)(many ? (rows + kMergeWarps - 1) / kMergeWarps : rows), 1, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L>, p) != cudaSuccess) return 5;
+  if ((many ? cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, 1>, p)
+            : cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, kMergeWarps>, p)) != cudaSuccess)
+    return 5;
   return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 
@@ -306,6 +330,10 @@ inline FwdCachePlan fwd_cache_plan(const CacheArgs &a, int rows, int granule, in
   x.ctas = x.most < most_ctas ? (int)x.most : most_ctas;
   return x;
 }
+// The kernel for many query rows (fa_fwd_cache_sm100.cu).
+FwdCachePlan fwd_cache_tile_plan(const CacheArgs &a);
+int launch_fwd_cache_tiles(const CacheArgs &a, const FwdCachePlan &x);
+
 inline size_t fwd_cache_plan_bytes(const FwdCachePlan &x, int d) {
   return (size_t)x.ctas * 2 * x.prows * (d + 1) * 4;
 }
