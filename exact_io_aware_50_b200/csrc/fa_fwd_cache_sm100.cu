@@ -6,7 +6,7 @@
 // (m for the sum of 2^{s - m}, M for the weights 2^{s - m} sv) and the same
 // roundings: q and the weights as halves, the codes exactly as halves.
 //
-// A CTA (one per SM, 12 warps) takes NT tiles of 128 rows of one key/value
+// A CTA (one per SM, 16 warps) takes NT tiles of 128 rows of one key/value
 // head, row r being query r / g of the group's head r % g, and blocks of 128
 // tokens of its run of the line:
 //   warps 0 .. 4 NT - 1  softmax and epilogue, a thread per row (TMEM lane)
@@ -14,7 +14,7 @@
 //                        registers a block ahead, and write halves into
 //                        128-byte-swizzled shared memory when the block before
 //                        has left it; tokens that do not exist become zeros
-//   warp 11              issues the MMAs (lane 0)
+//   warp 15              issues the MMAs (lane 0)
 // S_t = Q_t K^T lands in TMEM; the softmax thread reads its row, which frees S
 // for the next block's product, and writes the weights to shared memory; O_t +=
 // P_t V accumulates in TMEM.  All MMAs are kind::f16 with halves: M 128, N 128
@@ -28,8 +28,8 @@ namespace fa {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int kMmaWarp = 11;
-constexpr int kThreads = 384;
+constexpr int kMmaWarp = 15;
+constexpr int kThreads = 512;
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
 constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
@@ -193,13 +193,21 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       const int *tab = p.table + (long long)run.b * p.max_pages;
       // of a block's 16-token group `lane` (lanes 0 .. 7): the cache row of its
       // first token (rows of d codes), kNone: no page
+      // (Page numbers are fetched a block before they are looked at, scales a
+      // block before they are used, so that no load is waited for.)
       constexpr uint32_t kNone = 0xFFFFFFFFu;
-      auto lookup = [&](int j) {
+      constexpr int kNoToken = -2147483647 - 1;
+      auto fetch = [&](int j) {
         const int tok = (run.g0 + j) * BN + lane * 16;
-        if (lane >= 8 || j >= n || tok >= run.len) return kNone;
-        const int pg = checked_page(tab, tok >> p.page_log2, p.num_pages, p.err);
-        return pg < 0 ? kNone
-                      : (((uint32_t)pg * p.Hkv + run.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+        return lane >= 8 || j >= n || tok >= run.len ? kNoToken : tab[tok >> p.page_log2];
+      };
+      auto row_of = [&](int pg, int j) {
+        if ((unsigned)pg < (unsigned)p.num_pages) {
+          const int tok = (run.g0 + j) * BN + lane * 16;
+          return (((uint32_t)pg * p.Hkv + run.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
+        }
+        if (pg != kNoToken) atomicOr(p.err, kErrPage);
+        return kNone;
       };
       // this thread's chunks of K or V of block j, whose groups lie at `rows`
       auto load = [&](const uint8_t *cache, int j, uint32_t rows, uint4 (&x)[NL]) {
@@ -218,18 +226,25 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         for (int i = 0; i < NL; ++i)
           if (i * RPI + ct4 < ROWS) store_halves(my_dst + tile + i * RPI * 128, x[i]);
       };
-      // (sk, log2 sv) of a group; without a page (1, -inf): nothing visible
+      // (sk, sv) of a group; without a page (1, 0), whose log2 sv hides it
       auto scale_of = [&](uint32_t row) {
-        if (row == kNone) return make_float2(1.f, -INFINITY);
+        if (row == kNone) return make_float2(1.f, 0.f);
         const uint32_t i = row >> p.page_log2;
-        return make_float2(p.k_scale[i], log2f(p.v_scale[i]));
+        return make_float2(p.k_scale[i], p.v_scale[i]);
       };
       // ---- the first blocks' codes are on their way while q is converted
-      uint32_t pg0 = lookup(0), pg1 = lookup(1), pg2 = lookup(2);   // of blocks j, j + 1, j + 2
+      uint32_t row0, row1;   // of blocks j and j + 1
+      int pg2;               // of block j + 2
+      {
+        const int a0 = fetch(0), a1 = fetch(1);
+        pg2 = fetch(2);
+        row0 = row_of(a0, 0);
+        row1 = row_of(a1, 1);
+      }
       uint4 kr[NL], vr[NL];
-      load(p.k_cache, 0, pg0, kr);
-      load(p.v_cache, 0, pg0, vr);
-      float2 sc = scale_of(pg0);
+      load(p.k_cache, 0, row0, kr);
+      load(p.v_cache, 0, row0, vr);
+      float2 sc = scale_of(row0);
 
       // ---- q: 16 or 32 lanes a row (8 at d = 64), each row times a power of
       // two that brings its largest entry to [2^13, 2^14)
@@ -290,13 +305,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         if (j < n) {
           ok = warp_wait_all(bar(B_KEMPTY), ((g + j) & 1) ^ 1, wc);
           if (!ok) break;
-          if (ct < 8) scales[((g + j) & 3) * 8 + ct] = sc;
+          if (ct < 8) scales[((g + j) & 3) * 8 + ct] = make_float2(sc.x, log2f(sc.y));
           store(C::OFF_K, kr);
           fence_proxy_async_smem();
           mbar_arrive(bar(B_KFULL));
           if (j + 1 < n) {
-            load(p.k_cache, j + 1, pg1, kr);
-            sc = scale_of(pg1);
+            load(p.k_cache, j + 1, row1, kr);
+            sc = scale_of(row1);
           }
         }
         if (j > 0) {   // V of block j - 1
@@ -339,11 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           }
           fence_proxy_async_smem();
           mbar_arrive(bar(B_VFULL));
-          if (j < n) load(p.v_cache, j, pg0, vr);
+          if (j < n) load(p.v_cache, j, row0, vr);
         }
-        pg0 = pg1;
-        pg1 = pg2;
-        pg2 = lookup(j + 3);
+        row0 = row1;
+        row1 = row_of(pg2, j + 2);
+        pg2 = fetch(j + 3);
       }
       g += n;
     }
@@ -446,39 +461,44 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         if (!ok) break;
         tc_fence_after();
         if (j == 0) rc = row_c[t * BM + r];
-        uint32_t sr[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c)
-          tmem_ld32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bar(B_SEMPTY + t));   // the next block's S may take the columns
-        float *s = reinterpret_cast<float *>(sr);
+        // S is read in halves of 64 columns, so that a thread keeps to 128
+        // registers and the loops' code to the instruction cache: both for the
+        // maxima, then the second from registers and the first again.
         const float2 *scs = scales + ((g + j) & 3) * 8;
         const int col0 = x.token + j * BN;
-        // what the row does not see, or has no page: -inf
+        uint32_t sr[64];
+        float *s = reinterpret_cast<float *>(sr);
         bool whole = col0 + BN <= lim_warp;
 #pragma unroll
         for (int q = 0; q < 8; ++q) whole = whole && scs[q].y != -INFINITY;
-        if (!whole) {
+        auto read_half = [&](int h) {
+          tmem_ld32(ts + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_ld32(ts + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_wait_ld();
+          if (!whole) {   // what the row does not see, or has no page: -inf
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int seen = scs[q].y == -INFINITY ? 0 : lim - col0 - 16 * q;
+            for (int q = 0; q < 4; ++q) {
+              const int seen = scs[4 * h + q].y == -INFINITY ? 0 : lim - col0 - 64 * h - 16 * q;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[16 * q + e] = e < seen ? s[16 * q + e] : -INFINITY;
+              for (int e = 0; e < 16; ++e) s[16 * q + e] = e < seen ? s[16 * q + e] : -INFINITY;
+            }
           }
-        }
+        };
         // row maxima of s (base 2) and of s + log2 sv, by the pages' groups
         float mxs = -INFINITY, mxo = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          read_half(h);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 kv = scs[q];
-          float mx = s[16 * q];
+          for (int q = 0; q < 4; ++q) {
+            const float2 kv = scs[4 * h + q];
+            float mx = s[16 * q];
 #pragma unroll
-          for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[16 * q + e]);
-          mx *= fmaxf(rc * kv.x, kTiny);
-          mxs = fmaxf(mxs, mx);
-          mxo = fmaxf(mxo, mx + kv.y);
+            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[16 * q + e]);
+            mx *= fmaxf(rc * kv.x, kTiny);
+            mxs = fmaxf(mxs, mx);
+            mxo = fmaxf(mxo, mx + kv.y);
+          }
         }
         const bool moved = mxs > m_s + kLag || mxo > m_o + kLag;
         float al = 1.f, ao = 1.f;
@@ -494,32 +514,36 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         const bool none = m_s == -INFINITY;
         const float ms = none ? 0.f : m_s, diff = none ? 0.f : m_s - m_o + kShift;
         float sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 kv = scs[q];
-          const float cf = fmaxf(rc * kv.x, kTiny);
-          const float gain = fast_exp2(diff + kv.y);
-          uint32_t pk[8];
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float p0 = fast_exp2(fmaf(s[16 * q + 2 * e], cf, -ms));
-            const float p1 = fast_exp2(fmaf(s[16 * q + 2 * e + 1], cf, -ms));
-            part[e & 3] += p0 + p1;
-            pk[e] = pack_half2(p0 * gain, p1 * gain);
-          }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
-          if (q == 0 && g + j > 0) {   // P V of the block before is done with P
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+          if (h == 0) {
+            read_half(0);
+            tc_fence_before();
+            mbar_arrive(bar(B_SEMPTY + t));   // the next block's S may take the columns
+          } else if (g + j > 0) {             // P V of the block before is done with P
             ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
             tc_fence_after();
             if (!ok) break;
           }
-          // 16 columns = 32 bytes: two 16-byte units of the row
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int unit = 2 * q + k;
-            st_shared_v4(prow + (unit >> 3) * C::CHUNK + (((unit & 7) ^ (r & 7)) << 4), pk[4 * k], pk[4 * k + 1],
-                         pk[4 * k + 2], pk[4 * k + 3]);
+          for (int q = 0; q < 4; ++q) {
+            const float2 kv = scs[4 * h + q];
+            const float cf = fmaxf(rc * kv.x, kTiny);
+            const float gain = fast_exp2(diff + kv.y);
+            uint32_t pk[8];
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p0 = fast_exp2(fmaf(s[16 * q + 2 * e], cf, -ms));
+              const float p1 = fast_exp2(fmaf(s[16 * q + 2 * e + 1], cf, -ms));
+              part[e & 3] += p0 + p1;
+              pk[e] = pack_half2(p0 * gain, p1 * gain);
+            }
+            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            // 16 columns = 32 bytes: two 16-byte units of the row
+            const uint32_t at = prow + h * C::CHUNK + (((2 * q) ^ (r & 7)) << 4);
+            st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
+            st_shared_v4(at ^ 16, pk[4], pk[5], pk[6], pk[7]);
           }
         }
         l = l * al + sum;
