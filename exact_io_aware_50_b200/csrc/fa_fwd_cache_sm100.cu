@@ -9,11 +9,12 @@
 // A CTA (one per SM, 16 warps) takes NT tiles of 128 rows of one key/value
 // head, row r being query r / g of the group's head r % g, and blocks of 128
 // tokens of its run of the line:
-//   warps 0 .. 4 NT - 1  softmax and epilogue, a thread per row (TMEM lane)
-//   the others but one   converters: they read q rows and the pages' codes into
-//                        registers a block ahead, and write halves into
-//                        128-byte-swizzled shared memory when the block before
-//                        has left it; tokens that do not exist become zeros
+//   warps 0 .. 4 NT - 1  softmax and epilogue, a thread per row (TMEM lane);
+//                        they convert their rows of q first
+//   the others but one   converters: they read the pages' codes into registers a
+//                        block ahead, and write halves into 128-byte-swizzled
+//                        shared memory when the block before has left it; tokens
+//                        that do not exist become zeros
 //   warp 15              issues the MMAs (lane 0)
 // S_t = Q_t K^T lands in TMEM; the softmax thread reads its row, which frees S
 // for the next block's product, and writes the weights to shared memory; O_t +=
@@ -49,13 +50,12 @@ struct TileCfg {
   static constexpr int OFF_P = OFF_Q + NT * TILE;
   static constexpr int OFF_K = OFF_P + NT * P_TILE;
   static constexpr int OFF_V = OFF_K + TILE;
-  static constexpr int OFF_ROWC = OFF_V + TILE;       // [NT * 128] float: scale of a row's scores
-  static constexpr int OFF_SCALE = OFF_ROWC + NT * BM * 4;   // [4][8] (sk, log2 sv) of a block's 16-token groups
+  static constexpr int OFF_SCALE = OFF_V + TILE;             // [4][8] (sk, log2 sv) of a block's 16-token groups
   static constexpr int OFF_NAN = OFF_SCALE + 4 * 8 * 8;      // [2][D] first NaN token of a column
   static constexpr int OFF_ANY = OFF_NAN + 2 * D * 4;        // [2] whether there is one
   static constexpr int OFF_PIECE = OFF_ANY + 8;              // [2] Piece
   static constexpr int OFF_BAR = OFF_PIECE + 2 * 32;
-  static constexpr int NBAR = 11 + 6 * NT;
+  static constexpr int NBAR = 10 + 6 * NT;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;        // TMEM base, abort flag
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int TM_S = 0, TM_O = NT * BN;
@@ -92,6 +92,13 @@ __device__ __forceinline__ void store_halves(uint32_t at, const uint4 &codes) {
   st_shared_v4(at ^ 16, h[4], h[5], h[6], h[7]);
 }
 
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void store8(void *dst, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCacheParams p) {
   constexpr int D = C::D, NT = C::NT;
@@ -103,13 +110,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
   }
   launch_dependents();   // the merge kernel's CTAs may take their places
   auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
-  constexpr int B_UFULL = 0, B_UEMPTY = 2, B_QFULL = 4, B_QEMPTY = 5, B_KFULL = 6, B_KEMPTY = 7,
-                B_VFULL = 8, B_VEMPTY = 9, B_DRAIN = 10, B_SFULL = 11, B_SEMPTY = 11 + NT,
-                B_PFULL = 11 + 2 * NT, B_PEMPTY = 11 + 3 * NT, B_OFULL = 11 + 4 * NT,
-                B_OEMPTY = 11 + 5 * NT;
+  constexpr int B_UFULL = 0, B_UEMPTY = 2, B_QFULL = 4, B_KFULL = 5, B_KEMPTY = 6, B_VFULL = 7,
+                B_VEMPTY = 8, B_DRAIN = 9, B_SFULL = 10, B_SEMPTY = 10 + NT, B_PFULL = 10 + 2 * NT,
+                B_PEMPTY = 10 + 3 * NT, B_OFULL = 10 + 4 * NT, B_OEMPTY = 10 + 5 * NT;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
-  float *row_c = reinterpret_cast<float *>(smem + C::OFF_ROWC);
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE);
   // Two lists of NaN codes, for pieces in turn.  A piece's converters clear the
   // next piece's list before they hand over their last V.
@@ -122,8 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       mbar_init(bar(B_UFULL + i), 1);
       mbar_init(bar(B_UEMPTY + i), NT * BM + 1);   // softmax threads, the MMA issuer
     }
-    mbar_init(bar(B_QFULL), C::CT);
-    mbar_init(bar(B_QEMPTY), 1);
+    mbar_init(bar(B_QFULL), NT * BM);
     mbar_init(bar(B_KFULL), C::CT);
     mbar_init(bar(B_KEMPTY), 1);
     mbar_init(bar(B_VFULL), C::CT);
@@ -246,59 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       load(p.v_cache, 0, row0, vr);
       float2 sc = scale_of(row0);
 
-      // ---- q: 16 or 32 lanes a row (8 at d = 64), each row times a power of
-      // two that brings its largest entry to [2^13, 2^14)
-      ok = warp_wait_all(bar(B_QEMPTY), (u & 1) ^ 1, wc);
-      // the softmax has read row_c by the time it has read its last S
-      for (int t = 0; t < NT && ok && u > 0; ++t) ok = warp_wait_all(bar(B_SEMPTY + t), (g - 1) & 1, wc);
-      if (!ok) break;
-      int lim_min = run.len;   // tokens that every row of the piece sees
-      {
-        constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes of a row, rows of a warp at a time
-        constexpr int AHEAD = 4;
-        const int sub = lane / LPR, col = lane % LPR;
-        for (int r = (ct >> 5) * RPW; r < NT * BM; r += C::CONV * RPW * AHEAD) {
-          uint4 raw[AHEAD];
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k) {
-            const int row = r + k * C::CONV * RPW + sub, rr = run.r0 + row;
-            raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < NT * BM && rr < p.R) {
-              const int i = rr / group, hq = run.h * group + rr - i * group;
-              raw[k] = *reinterpret_cast<const uint4 *>(
-                  p.q + (((long long)run.b * p.Hq + hq) * p.Nq + i) * D + col * 8);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k) {
-            const int row = r + k * C::CONV * RPW + sub;
-            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-#pragma unroll
-            for (int off = LPR / 2; off > 0; off >>= 1)
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
-            const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-            if (row < NT * BM) {
-              if (col == 0)
-                row_c[row] = p.scale_log2 * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
-              uint32_t h[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                h[i] = pack_half2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-              st_shared_v4(sbase + C::OFF_Q + (row >> 7) * C::TILE + (col >> 3) * C::CHUNK + (row & 127) * 128 +
-                               (((col & 7) ^ (row & 7)) << 4),
-                           h[0], h[1], h[2], h[3]);
-            }
-          }
-        }
-        if (p.causal) lim_min = max(0, min(run.len, run.len - p.Nq + run.r0 / group + 1));
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(B_QFULL));
+      // tokens that every row of the piece sees
+      const int lim_min = p.causal ? max(0, min(run.len, run.len - p.Nq + run.r0 / group + 1)) : run.len;
 
       for (int j = 0; j <= n && ok; ++j) {
         // K runs a block ahead of V
@@ -399,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         }
         if (!ok) break;
         mma_commit(bar(B_KEMPTY));
-        if (n == 1) mma_commit(bar(B_QEMPTY));
         for (int j = 0; j < n && ok; ++j) {
           const int gj = g + j;
           if (j + 1 < n) {
@@ -413,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
             }
             if (!ok) break;
             mma_commit(bar(B_KEMPTY));
-            if (j + 2 == n) mma_commit(bar(B_QEMPTY));
           }
           ok = bounded_wait(bar(B_VFULL), gj & 1, wc);
           for (int t = 0; t < NT && ok; ++t) {
@@ -455,12 +406,61 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       // tokens [0, lim) visible; the warp's least, for whole blocks
       const int lim = !live ? x.len : (p.causal ? max(0, min(x.len, x.len - p.Nq + i + 1)) : x.len);
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
-      float m_s = -INFINITY, m_o = -INFINITY, l = 0.f, rc = 0.f;
+      const long long row = ((long long)x.b * p.Hq + hq) * p.Nq + i;   // of q, o, lse
+      float m_s = -INFINITY, m_o = -INFINITY, l = 0.f;
+
+      // ---- q: the warp converts its 32 rows (D / 8 lanes a row), each times a
+      // power of two that brings its largest entry to [2^13, 2^14).  The tile is
+      // free: this warp has seen the last S of the piece before.
+      float rc = 0.f;   // this row's scale * log2 e / that power of two
+      {
+        constexpr int LPR = D / 8, RPW = 32 / LPR, AHEAD = 8;   // lanes of a row, rows at a time, loads in flight
+        const int sub = lane / LPR, col = lane % LPR;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += RPW * AHEAD) {
+          uint4 raw[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            // the row's place in memory lies with the thread whose row it is
+            const int lr = r0 + k * RPW + sub;
+            const long long at = __shfl_sync(0xffffffffu, live ? row : -1, lr & 31);
+            raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (lr < 32 && at >= 0) raw[k] = *reinterpret_cast<const uint4 *>(p.q + at * D + col * 8);
+          }
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const int lr = r0 + k * RPW + sub, tr = (warp & 3) * 32 + lr;   // row of the warp, of the tile
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            float mx = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
+            const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+            const float down = p.scale_log2 * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+            // lane of row r0 + k * RPW + i takes group i's factor
+            const int i = lane - (r0 + k * RPW);
+            const float got = __shfl_sync(0xffffffffu, down, (i & (RPW - 1)) * LPR);
+            if (i >= 0 && i < RPW) rc = got;
+            if (lr >= 32) continue;
+            uint32_t h[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              h[b] = pack_half2(__uint_as_float(w[b] << 16) * up, __uint_as_float(w[b] & 0xFFFF0000u) * up);
+            st_shared_v4(sbase + C::OFF_Q + t * C::TILE + (col >> 3) * C::CHUNK + tr * 128 + (((col & 7) ^ (tr & 7)) << 4),
+                         h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(B_QFULL));
+      }
+
       for (int j = 0; j < x.blocks; ++j) {
         ok = warp_wait_all(bar(B_SFULL + t), (g + j) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        if (j == 0) rc = row_c[t * BM + r];
         // S is read in halves of 64 columns, so that a thread keeps to 128
         // registers and the loops' code to the instruction cache: both for the
         // maxima, then the second from registers and the first again.
@@ -571,7 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       const bool seen = !(l == 0.f);
       const float f = seen ? fast_exp2(m_o - kShift - m_s) / l : 0.f;
       const bool nans = nan_any[u & 1] != 0;
-      const long long row = ((long long)x.b * p.Hq + hq) * p.Nq + i;
       const long long prt = x.part < 0 ? 0 : (long long)(x.part + t * BM + r);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -588,15 +587,17 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         }
         if (!live) continue;
         if (x.part < 0) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+          // (rows of o are 16-byte aligned only: the caller's pointer may be)
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * D + c * 32);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(p.o_part + prt * D + c * 32);
+          float *dst = p.o_part + prt * D + c * 32;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) store8(dst + 8 * e, &ov[8 * e]);
         }
       }
       if (live) {

@@ -120,16 +120,34 @@ struct Run {
   int h, r0, g0, g1, ng, len, stop;
 
   __device__ __forceinline__ bool start(const FwdCacheParams &p) {
+    const int lane = threadIdx.x & 31;
+    if (p.B <= 32) {   // one look at the lengths
+      const int n = lane < p.B ? L::head(p, L::len(p, lane)) : 0;
+      int inc = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      if (!cut(p, __shfl_sync(0xffffffffu, inc, 31))) return false;
+      const unsigned past = __ballot_sync(0xffffffffu, pos < inc * p.Hkv);   // not empty: pos < the total
+      b = __ffs(past) - 1;
+      b_first = __shfl_sync(0xffffffffu, inc - n, b) * p.Hkv;
+      return true;
+    }
     int total, unused;
     L::sums(p, 0, &total, &unused);
-    total *= p.Hkv;
-    const int per = (total + p.ctas - 1) / p.ctas;
-    pos = per * (int)blockIdx.x;      // at most total + per
-    end = min(total, pos + per);
-    if (pos >= end) return false;
+    if (!cut(p, total)) return false;
     b = L::sequence_at(p, pos / p.Hkv, &b_first);
     b_first *= p.Hkv;
     return true;
+  }
+  // [pos, end) of a line of `head` granules a head
+  __device__ __forceinline__ bool cut(const FwdCacheParams &p, int head) {
+    const int total = head * p.Hkv, per = (total + p.ctas - 1) / p.ctas;
+    pos = per * (int)blockIdx.x;      // at most total + per
+    end = min(total, pos + per);
+    return pos < end;
   }
   __device__ __forceinline__ bool next(const FwdCacheParams &p) {
     if (pos >= end) return false;
