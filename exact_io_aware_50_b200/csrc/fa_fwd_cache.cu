@@ -566,9 +566,15 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   return launch_fwd_cache_merge<D, RowLine>(p, a.stream);
 }
 
-// One tile of 16 rows: the kernel of this file; more rows read the cache once
-// for 128 of them on tcgen05.
-bool few_rows(const CacheArgs &a) { return (double)(a.Hq / a.Hkv) * a.Nq <= RowLine::ROWS; }
+// Up to three tiles of 16 rows (two at d = 256) go to the kernel of this file,
+// which reads the cache (L2, mostly) for each; more rows read it once for 128 of
+// them on tcgen05 (fa_fwd_cache_sm100.cu).  Measured on B200, us a call here /
+// there, B 32, 8000 tokens, 2 key/value heads: d = 64, 40 rows 52.5 / 85.5, 96 rows
+// 96.7 / 91.6; d = 128, 40 rows 74.5 / 80.6, 64 rows 95.8 / 85.6; d = 256, 32 rows
+// 96.6 / 116, 40 rows 126 / 121.
+bool few_rows(const CacheArgs &a) {
+  return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 256 ? 2 : 3) * RowLine::ROWS;
+}
 
 FwdCachePlan plan_of(const CacheArgs &a) {
   return few_rows(a) ? fwd_cache_plan(a, RowLine::ROWS, kGranule, kMaxCtas) : fwd_cache_tile_plan(a);

@@ -198,9 +198,9 @@ __device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
 }
 
 // Joins the pieces of the units that several CTAs covered: W warps of a
-// CTA of kMergeWarps take one query row.  W is kMergeWarps where rows are few
-// and pieces many, 1 where there are rows enough.  Rows of tiles that see no
-// token become O = 0, L = -inf.
+// CTA of kMergeWarps take one query row.  W is kMergeWarps where a unit has many
+// pieces, 1 where it has few (a warp has eight in flight).  Rows of tiles that see
+// no token become O = 0, L = -inf.
 constexpr int kMergeWarps = 8;
 
 template <int D, class L, int W>
@@ -236,20 +236,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k)
     if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
-  float top = -INFINITY, sum = 0.f;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
+  // lane i looks at pieces i, i + 32, ...
+  const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
+  float top = mine;
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float own = 0.f;   // lane i: the weight of piece i (W == 1: the first 32)
-  for (int i = lane; i < n; i += 32) {
+  const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
+  float sum = own;
+  if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
+  for (int i = lane + 32; i < n; i += 32) {
     const float x = p.l_part[at(i)];
     const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
     sum += w;
-    if (W > 1) {
-      if (i % W == warp) s_w[i] = w;   // each warp keeps its own pieces' weights
-    } else if (i < 32) {
-      own = w;
-    }
+    if (W > 1 && i % W == warp) s_w[i] = w;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -314,8 +314,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const
 // then wait for the main kernel's end.
 template <int D, class L>
 int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.Hq * p.Nq;
-  const bool many = rows > 1184;   // a warp a row fills the GPU's first 148 CTAs of eight
+  const long long rows = (long long)p.B * p.Hq * p.Nq, units = (long long)p.B * p.Hkv * p.tiles;
+  // a warp a row: about eight pieces a unit, or fewer, or rows enough to fill the GPU
+  const bool many = units * 8 >= p.ctas || rows > 148 * kMergeWarps;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
