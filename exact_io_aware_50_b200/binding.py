@@ -26,6 +26,7 @@ FA_ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libfa.so")
 _lib = None
+_torch = None   # the torch module, once a wrapper of the serving operators has run
 
 EXPORTS = ("fa_fwd", "fa_fwd_pair", "fa_fwd_fp8", "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_splitkv",
            "fa_fwd_splitkv_num_splits",
@@ -296,13 +297,6 @@ def _check_cuda(where, q, *others):
     library launches on the current device, which the wrappers set to q's
     (``_on``), so a tensor on another GPU would be read by kernels running on
     the wrong one."""
-    dev = q.device
-    if q.is_cuda and q.is_contiguous():
-        for t in others:
-            if t.device != dev or not t.is_contiguous():
-                break
-        else:
-            return
     for t in (q,) + others:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{where}: inputs must be contiguous CUDA tensors")
@@ -334,19 +328,42 @@ def _workspace(where, workspace, B, Hq, Nq, d, device):
     return workspace
 
 
-def _call(fn, name, t, *args):
-    """fn(*args, stream) on t's device and that device's current stream; raises
-    FaError.  The context switch and the stream object are skipped where the
-    device is current already: a decode step's calls are as short as this."""
-    import torch
-    dev = t.device.index
-    if torch.cuda.current_device() == dev:
+# The serving operators' wrappers are called once a layer and token, so they
+# keep their own time down: torch is imported once, the context switch and the
+# stream object are skipped where the device is current already.
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _call(fn, name, dev, *args):
+    """fn(*args, stream) on CUDA device number `dev` and its current stream;
+    raises FaError."""
+    torch = _torch
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, name)
+
+
+def _check_place(where, ref, others):
+    """ref and others: contiguous CUDA tensors on one device, as _check_cuda
+    asks, found in one pass where they are.  Returns the device's number."""
+    dev = ref.device
+    if dev.type == "cuda" and ref.is_contiguous():
+        for t in others:
+            if t.device != dev or not t.is_contiguous():
+                break
+        else:
+            return dev.index
+    _check_cuda(where, ref, *others)
+    return dev.index
 
 
 def _shape(q, k):
@@ -512,36 +529,41 @@ def rope_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=
 
 
 def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
-    import torch
-    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float32):
+    torch = _t()
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 4 or (dtype is not torch.bfloat16 and dtype is not torch.float32):
         raise ValueError(f"{where}: q must be [B, Hq, N, d], bfloat16 or float32")
-    B, Hq, N, d = q.shape
+    B, Hq, N, d = shape
     Hkv = 0
     if k is not None:
-        if (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != N
-                or k.shape[3] != d):
+        ks = k.shape
+        if len(ks) != 4 or k.dtype is not dtype or ks[0] != B or ks[2] != N or ks[3] != d:
             raise ValueError(f"{where}: k must be [B, Hkv, N, d] of q's dtype")
-        Hkv = k.shape[1]
-    per_batch = positions.dim() == 2
-    if (positions.dtype != torch.int32
-            or tuple(positions.shape) != ((B, N) if per_batch else (N,))):
+        Hkv = ks[1]
+    ps = positions.shape
+    per_batch = len(ps) == 2
+    if positions.dtype is not torch.int32 or ps != ((B, N) if per_batch else (N,)):
         raise ValueError(f"{where}: positions must be int32 [B, N] or [N]")
-    if freqs.dim() != 1 or freqs.dtype != torch.float64:
+    fs = freqs.shape
+    if len(fs) != 1 or freqs.dtype is not torch.float64:
         raise ValueError(f"{where}: freqs must be float64 [rot_dim / 2]")
-    if out is None:
-        qo = torch.empty_like(q)
-        ko = None if k is None else torch.empty_like(k)
-    else:
+    place = [positions, freqs] if k is None else [k, positions, freqs]
+    if out is not None:
         qo, ko = out
         for t, o in ((q, qo), (k, ko)):
             if (o is None) != (t is None) or (t is not None and (o.shape != t.shape
                                                                  or o.dtype != t.dtype)):
                 raise ValueError(f"{where}: out must be shaped and typed like (q, k)")
-    _check_cuda(where, q, positions, freqs, qo, *(() if k is None else (k, ko)))
-    name = name if q.dtype == torch.bfloat16 else name + "_f32"
-    _call(getattr(lib(), name), name, q, q.data_ptr(), 0 if k is None else k.data_ptr(),
+        place += [qo] if ko is None else [qo, ko]
+    dev = _check_place(where, q, place)
+    if out is None:   # contiguous, as q and k are
+        qo = torch.empty_like(q)
+        ko = None if k is None else torch.empty_like(k)
+    if dtype is torch.float32:
+        name += "_f32"
+    _call(getattr(_lib or lib(), name), name, dev, q.data_ptr(), 0 if k is None else k.data_ptr(),
           qo.data_ptr(), 0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
-          B, Hq, Hkv, N, d, 2 * freqs.shape[0], int(per_batch), int(interleaved), float(mscale))
+          B, Hq, Hkv, N, d, 2 * fs[0], per_batch, interleaved, mscale)
     return qo, ko
 
 
@@ -560,35 +582,30 @@ def rope_backward(dq, dk, positions, freqs, mscale=1.0, interleaved=False, out=N
                  "fa_rope_bwd")
 
 
-def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, d, *more):
-    """The cache's tensors against B, Hkv, d.  `more`: (name, int32 [B] tensor
-    or None) pairs, or tensors whose place alone is checked.  Returns (page,
-    num_pages, max_pages)."""
-    import torch
-    f8 = (torch.uint8, torch.float8_e4m3fn)
+def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, d, name,
+                 lens, *more):
+    """The cache's tensors against B, Hkv, d; lens (called `name`): int32 [B];
+    more: tensors whose place alone is checked.  Returns (page, num_pages,
+    max_pages, device number)."""
+    torch = _torch
+    f8 = (torch.float8_e4m3fn, torch.uint8)
     shape = k_cache.shape
     if (len(shape) != 4 or shape[1] != Hkv or shape[3] != d or v_cache.shape != shape
             or k_cache.dtype not in f8 or v_cache.dtype not in f8):
         raise ValueError(f"{where}: k_cache and v_cache must be E4M3 [num_pages, Hkv, page, d]")
     num_pages, _, page, _ = shape
     shape = (num_pages, Hkv)
-    if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype != torch.float32
-            or v_scale.dtype != torch.float32):
+    f32, i32 = torch.float32, torch.int32
+    if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype is not f32
+            or v_scale.dtype is not f32):
         raise ValueError(f"{where}: k_scale and v_scale must be float32 [num_pages, Hkv]")
     shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B or block_table.dtype != torch.int32:
+    if len(shape) != 2 or shape[0] != B or block_table.dtype is not i32:
         raise ValueError(f"{where}: block_table must be int32 [B, max_pages]")
-    place = [k_cache, v_cache, k_scale, v_scale, block_table]
-    for x in more:
-        if isinstance(x, tuple):
-            name, x = x
-            if x is None:
-                continue
-            if x.shape != (B,) or x.dtype != torch.int32:
-                raise ValueError(f"{where}: {name} must be int32 [B]")
-        place.append(x)
-    _check_cuda(where, ref, *place)
-    return page, num_pages, shape[1]
+    if lens is None or lens.shape != (B,) or lens.dtype is not i32:
+        raise ValueError(f"{where}: {name} must be int32 [B]")
+    dev = _check_place(where, ref, (k_cache, v_cache, k_scale, v_scale, block_table, lens) + more)
+    return page, num_pages, shape[1], dev
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None):
@@ -597,18 +614,22 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, c
     power-of-two scale per page and head (fa_cache_append).  count: int32 [B]
     tokens of each sequence that count (None: all T).  The cache tensors are
     updated in place."""
-    import torch
-    if (k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype
-            or k.dtype not in (torch.bfloat16, torch.float32)):
+    torch = _t()
+    shape, dtype = k.shape, k.dtype
+    if (len(shape) != 4 or v.shape != shape or v.dtype is not dtype
+            or (dtype is not torch.bfloat16 and dtype is not torch.float32)):
         raise ValueError("cache_append: k and v must both be [B, Hkv, T, d], bfloat16 or float32")
-    B, Hkv, T, d = k.shape
-    if start is None:
-        raise ValueError("cache_append: start must be int32 [B]")
-    page, num_pages, max_pages = _check_cache("cache_append", k, k_cache, v_cache, k_scale, v_scale,
-                                              block_table, B, Hkv, d, ("start", start),
-                                              ("count", count), v)
-    name = "fa_cache_append" if k.dtype == torch.bfloat16 else "fa_cache_append_f32"
-    _call(getattr(lib(), name), name, k, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+    B, Hkv, T, d = shape
+    more = (v,)
+    if count is not None:
+        if count.shape != (B,) or count.dtype is not torch.int32:
+            raise ValueError("cache_append: count must be int32 [B]")
+        more = (v, count)
+    page, num_pages, max_pages, dev = _check_cache("cache_append", k, k_cache, v_cache, k_scale,
+                                                   v_scale, block_table, B, Hkv, d, "start", start,
+                                                   *more)
+    name = "fa_cache_append_f32" if dtype is torch.float32 else "fa_cache_append"
+    _call(getattr(_lib or lib(), name), name, dev, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
           start.data_ptr(), 0 if count is None else count.data_ptr(), B, Hkv, T, d, page,
           num_pages, max_pages)
@@ -618,21 +639,22 @@ def cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, N, dtype=N
     """Dense k, v [B, Hkv, N, d] (bfloat16, or dtype=torch.float32): the first
     N tokens of each sequence out of the cache, zeros from lens[b] on
     (fa_cache_read)."""
-    import torch
+    torch = _t()
     dtype = torch.bfloat16 if dtype is None else dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("cache_read: dtype must be bfloat16 or float32")
-    if k_cache.dim() != 4 or block_table.dim() != 2 or lens is None:
+    if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("cache_read: k_cache must be [num_pages, Hkv, page, d], block_table "
-                         "int32 [B, max_pages], lens int32 [B]")
+                         "int32 [B, max_pages]")
     _, Hkv, _, d = k_cache.shape
     B = block_table.shape[0]
-    page, num_pages, max_pages = _check_cache("cache_read", k_cache, k_cache, v_cache, k_scale,
-                                              v_scale, block_table, B, Hkv, d, ("lens", lens))
-    k = torch.empty(B, Hkv, N, d, device=k_cache.device, dtype=dtype)
+    page, num_pages, max_pages, dev = _check_cache("cache_read", k_cache, k_cache, v_cache,
+                                                   k_scale, v_scale, block_table, B, Hkv, d,
+                                                   "lens", lens)
+    k = torch.empty((B, Hkv, N, d), device=k_cache.device, dtype=dtype)
     v = torch.empty_like(k)
-    name = "fa_cache_read" if dtype == torch.bfloat16 else "fa_cache_read_f32"
-    _call(getattr(lib(), name), name, k_cache, k_cache.data_ptr(), v_cache.data_ptr(),
+    name = "fa_cache_read_f32" if dtype is torch.float32 else "fa_cache_read"
+    _call(getattr(_lib or lib(), name), name, dev, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
           k.data_ptr(), v.data_ptr(), B, Hkv, N, d, page, num_pages, max_pages)
     return k, v
@@ -644,32 +666,31 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     first lens[b] tokens of each sequence of the paged E4M3 cache
     (fa_fwd_cache).  Causal is bottom-right aligned: the queries are the last
     Nq of those tokens.  A query that sees no key gets O = 0, L = -inf."""
-    import torch
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or k_cache.dim() != 4:
+    torch = _t()
+    shape = q.shape
+    if len(shape) != 4 or q.dtype is not torch.bfloat16 or k_cache.dim() != 4:
         raise ValueError("forward_cache: q must be bfloat16 [B, Hq, Nq, d], k_cache "
                          "[num_pages, Hkv, page, d]")
-    B, Hq, Nq, d = q.shape
+    B, Hq, Nq, d = shape
     Hkv = k_cache.shape[1]
-    if lens is None:
-        raise ValueError("forward_cache: lens must be int32 [B]")
-    page, num_pages, max_pages = _check_cache("forward_cache", q, k_cache, v_cache, k_scale,
-                                              v_scale, block_table, B, Hkv, d, ("lens", lens))
-    scale = d ** -0.5 if scale is None else float(scale)
-    need = int(lib().fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages))
+    page, num_pages, max_pages, dev = _check_cache("forward_cache", q, k_cache, v_cache, k_scale,
+                                                   v_scale, block_table, B, Hkv, d, "lens", lens)
+    L = _lib or lib()
+    place = q.device
+    need = L.fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages)
     if workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8) if need else None
+        workspace = torch.empty(need, device=place, dtype=torch.uint8)
     elif (not workspace.is_cuda or not workspace.is_contiguous()
           or workspace.numel() * workspace.element_size() < need):
         raise ValueError(f"forward_cache: workspace must be a contiguous CUDA buffer of at least "
                          f"{need} bytes")
-    elif workspace.device != q.device:
-        raise ValueError(f"forward_cache: workspace must be on q's device ({q.device}); "
+    elif workspace.device != place:
+        raise ValueError(f"forward_cache: workspace must be on q's device ({place}); "
                          f"got {workspace.device}")
     o = torch.empty_like(q)
-    L = torch.empty(B, Hq, Nq, device=q.device, dtype=torch.float32)
-    _call(lib().fa_fwd_cache, "fa_fwd_cache", q, q.data_ptr(), k_cache.data_ptr(),
+    lse = torch.empty((B, Hq, Nq), device=place, dtype=torch.float32)
+    _call(L.fa_fwd_cache, "fa_fwd_cache", dev, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-          lens.data_ptr(), o.data_ptr(), L.data_ptr(),
-          0 if workspace is None else workspace.data_ptr(), B, Hq, Hkv, Nq, d, page, num_pages,
-          max_pages, scale, int(causal))
-    return o, L
+          lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
+          page, num_pages, max_pages, d ** -0.5 if scale is None else scale, causal)
+    return o, lse

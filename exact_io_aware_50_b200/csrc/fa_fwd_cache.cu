@@ -559,8 +559,8 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   using C = RowCfg<D>;
   const FwdCacheParams p = fwd_cache_params(a, x);
   auto kern = fwd_cache_rows_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return 5;
+  static unsigned long long allowed = 0;
+  if (!allow_smem(kern, C::SMEM, &allowed)) return 5;
   kern<<<x.ctas, kWarps * 32, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
   return launch_fwd_cache_merge<D, RowLine>(p, a.stream);

@@ -624,7 +624,8 @@ template <class C>
 int run_tiles(const CacheArgs &a, const FwdCachePlan &x) {
   const FwdCacheParams p = fwd_cache_params(a, x);
   auto kern = fwd_cache_tile_kernel<C>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return 5;
+  static unsigned long long allowed = 0;
+  if (!allow_smem(kern, C::SMEM, &allowed)) return 5;
   kern<<<x.ctas, kThreads, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
   return launch_fwd_cache_merge<C::D, typename C::L>(p, a.stream);

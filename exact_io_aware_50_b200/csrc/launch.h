@@ -64,6 +64,20 @@ inline size_t splitkv_ws_bytes(int splits, int B, int Hq, int Nq, int d) {
   return splitkv_l_offset(splits, B, Hq, Nq, d) + (size_t)splits * B * Hq * Nq * 4;
 }
 
+// Lets `kern` use `bytes` of dynamic shared memory on the current device, asked
+// for once a device: *done holds a bit for each.
+template <class K>
+inline bool allow_smem(K kern, int bytes, unsigned long long *done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  const unsigned long long bit = 1ull << dev;
+  if (__atomic_load_n(done, __ATOMIC_RELAXED) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
+  return true;
+}
+
 // Status codes use the fa_status numbering of fa.h.
 int launch_fwd_f32(const AttnArgs &a);
 int launch_bwd_f32(const AttnArgs &a);
