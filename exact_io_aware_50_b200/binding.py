@@ -563,7 +563,7 @@ def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
         name += "_f32"
     _call(getattr(_lib or lib(), name), name, dev, q.data_ptr(), 0 if k is None else k.data_ptr(),
           qo.data_ptr(), 0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
-          B, Hq, Hkv, N, d, 2 * fs[0], per_batch, interleaved, mscale)
+          B, Hq, Hkv, N, d, 2 * fs[0], per_batch, 1 if interleaved else 0, mscale)
     return qo, ko
 
 
@@ -692,5 +692,6 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     _call(L.fa_fwd_cache, "fa_fwd_cache", dev, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
           lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
-          page, num_pages, max_pages, d ** -0.5 if scale is None else scale, causal)
+          page, num_pages, max_pages, d ** -0.5 if scale is None else scale,
+          1 if causal else 0)
     return o, lse

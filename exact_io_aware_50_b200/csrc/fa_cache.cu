@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs a) {
 template <class T>
 int run_append(const CacheArgs &a) {
   const long long pages = ((long long)a.T + a.page - 2) / a.page + 1;   // touched, at most
-  if ((long long)a.B * a.Hkv > 65535) return 2;
   const dim3 grid((unsigned)pages, (unsigned)(a.B * a.Hkv), 2);
   // A page's new tokens are at most min(T, page): 8 to 8192 chunks of 16 bytes.
   // A thread holds eight of them, so that small CTAs keep many loads in flight
@@ -203,7 +202,6 @@ int run_append(const CacheArgs &a) {
 
 template <class T>
 int run_read(const CacheArgs &a) {
-  if ((long long)a.B * a.Hkv > 65535) return 2;
   const int rows = 256 / (a.d * (int)sizeof(T) / 16) * kReads;
   const dim3 grid((unsigned)((a.T + rows - 1) / rows), (unsigned)(a.B * a.Hkv));
   cache_read_kernel<T><<<grid, 256, 0, a.stream>>>(a);

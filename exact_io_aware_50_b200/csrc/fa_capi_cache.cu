@@ -49,7 +49,7 @@ int check_cache(const CacheArgs &a, int tokens) {
       (double)a.B * a.Hkv > (double)(1 << 28) || (double)a.num_pages * a.Hkv > 2147483647.0 ||
       (double)a.B * a.max_pages > 2147483647.0 ||
       (double)a.B * a.Hkv * tokens * a.d > 4.0e12 ||
-      (double)a.num_pages * a.Hkv * a.page * a.d > 4.0e12)
+      (double)a.num_pages * a.Hkv * a.page > 4294967294.0)   // cache rows, in uint32
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -75,6 +75,7 @@ int run_append(CacheArgs &a) {
     if (!p) return FA_ERR_INVALID_ARG;
   int st = check_cache(a, a.T);
   if (st) return st;
+  if ((double)a.B * a.Hkv > 65535.0) return FA_ERR_UNSUPPORTED;   // a grid dimension
   if (!cache_aligned(a)) return FA_ERR_ALIGNMENT;
   if ((st = prologue(a))) return st;
   return launch_cache_append(a);
@@ -87,6 +88,7 @@ int run_read(CacheArgs &a) {
     if (!p) return FA_ERR_INVALID_ARG;
   int st = check_cache(a, a.T);
   if (st) return st;
+  if ((double)a.B * a.Hkv > 65535.0) return FA_ERR_UNSUPPORTED;   // a grid dimension
   if (!cache_aligned(a)) return FA_ERR_ALIGNMENT;
   if ((st = prologue(a))) return st;
   return launch_cache_read(a);
@@ -204,7 +206,7 @@ FA_EXPORT int fa_fwd_cache(const void *q, const void *k_cache, const void *v_cac
   int st = fa::check_cache(a, Nq);
   if (st) return st;
   if (Hq <= 0 || Hq % Hkv || !(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
-  if ((double)B * Hq * Nq > 2147483647.0 || (double)B * Hq * Nq * d > 4.0e12)
+  if ((double)B * Hq * Nq > 2147483647.0 || fa::fwd_cache_granules(a) > 2.0e9)
     return FA_ERR_UNSUPPORTED;
   const bool need_ws = fa::fwd_cache_ws_bytes(a) > 0;
   if (need_ws && !workspace) return FA_ERR_INVALID_ARG;

@@ -583,16 +583,11 @@ FwdCachePlan plan_of(const CacheArgs &a) {
 }  // namespace
 
 size_t fwd_cache_ws_bytes(const CacheArgs &a) { return fwd_cache_plan_bytes(plan_of(a), a.d); }
+double fwd_cache_granules(const CacheArgs &a) { return plan_of(a).most; }
 
 int launch_fwd_cache(const CacheArgs &a) {
   const FwdCachePlan x = plan_of(a);
-  // the line's granules are counted in int32
-  if (x.R > 2147483647.0 || x.most > 2.0e9) return 2;
-  if (!few_rows(a)) {
-    // cache rows (of d codes) are counted in uint32 there
-    if ((double)a.num_pages * a.Hkv * a.page >= 4294967295.0) return 2;
-    return launch_fwd_cache_tiles(a, x);
-  }
+  if (!few_rows(a)) return launch_fwd_cache_tiles(a, x);
   switch (a.d) {
     case 64: return run_rows<64>(a, x);
     case 128: return run_rows<128>(a, x);

@@ -124,7 +124,10 @@ struct CacheArgs {
 int launch_cache_append(const CacheArgs &a);
 int launch_cache_read(const CacheArgs &a);
 int launch_fwd_cache(const CacheArgs &a);
-size_t fwd_cache_ws_bytes(const CacheArgs &a);   // by B, Hq, Hkv, Nq, d, page, max_pages
+// By B, Hq, Hkv, Nq, d, page, max_pages: workspace bytes; pieces of work when every
+// sequence fills its table (counted in int32 by the kernels).
+size_t fwd_cache_ws_bytes(const CacheArgs &a);
+double fwd_cache_granules(const CacheArgs &a);
 
 // Argument checks and per-call device set-up shared by the C entry points
 // (fa_status codes): size/scale rules, then current device, architecture and

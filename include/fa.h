@@ -291,8 +291,8 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o,
  * (in place); it must not overlap it otherwise.
  * positions: int32 in device memory, [B, N] (pos_per_batch != 0) or [N]
  * shared by the batch; any value, negative ones included.
- * freqs: float64 [rot_dim / 2] in device memory (fa_rope_freqs fills such a
- * table on the host).  mscale: finite and > 0, else FA_ERR_INVALID_ARG.
+ * freqs: finite float64 [rot_dim / 2] in device memory (fa_rope_freqs fills
+ * such a table on the host).  mscale: finite and > 0, else FA_ERR_INVALID_ARG.
  * d: a multiple of 4, at most 256; rot_dim: a multiple of 8, at most d
  * (FA_ERR_UNSUPPORTED otherwise).
  *
@@ -369,8 +369,9 @@ int fa_rope_freqs(double *freqs, float *mscale, int rot_dim, double theta, int k
  * rounded again.  New codes are E4M3(x / scale), round to nearest even;
  * infinities become +-448, NaN stays NaN.  Slots behind the last new token
  * keep their bytes.
- * No page may be written for two sequences, or twice, in one call (the result
- * is then undefined).
+ * No page may be written for two sequences, or twice, in one call (that page's
+ * codes and scale are then undefined).  B * Hkv is at most 65535
+ * (FA_ERR_UNSUPPORTED; the same for fa_cache_read).
  *
  * fa_cache_read -- the first N tokens of each sequence back as dense k, v
  * [B, Hkv, N, d], bfloat16 (fa_cache_read: scale * code rounded to nearest

@@ -80,6 +80,7 @@ def test_append_argument_errors(fn):
     for i in range(8):   # the ninth, count, may be null
         assert call(ptrs=tuple(0 if j == i else FAKE for j in range(9))) == F.FA_ERR_INVALID_ARG
     _size_errors(call)
+    assert call(B=256, Hkv=257) == F.FA_ERR_UNSUPPORTED
     for i in range(9):
         off = 8 if i < 4 else 2
         assert call(ptrs=tuple(FAKE + off if j == i else FAKE for j in range(9))) == F.FA_ERR_ALIGNMENT
@@ -94,6 +95,7 @@ def test_read_argument_errors(fn):
     for i in range(8):
         assert call(ptrs=tuple(0 if j == i else FAKE for j in range(8))) == F.FA_ERR_INVALID_ARG
     _size_errors(call)
+    assert call(B=256, Hkv=257) == F.FA_ERR_UNSUPPORTED
     for i, off in ((0, 8), (1, 8), (2, 2), (3, 2), (4, 2), (5, 2), (6, 8), (7, 8)):
         assert call(ptrs=tuple(FAKE + off if j == i else FAKE for j in range(8))) == F.FA_ERR_ALIGNMENT
 
@@ -107,6 +109,8 @@ def test_forward_cache_argument_errors():
     for i in range(9):
         assert call(ptrs=tuple(0 if j == i else FAKE for j in range(10))) == F.FA_ERR_INVALID_ARG
     _size_errors(call)
+    # more pieces of work than int32 counts, were every sequence to fill its table
+    assert call(B=1024, Hkv=1024, Hq=1024, max_pages=2**20) == F.FA_ERR_UNSUPPORTED
     for kw in (dict(Hq=3), dict(Hq=0), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf"))):
         assert call(**kw) == F.FA_ERR_INVALID_ARG, kw
     for i in range(9):

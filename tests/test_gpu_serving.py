@@ -385,6 +385,65 @@ def test_attention_sharp_and_rising_scores():
         check_attention(q.to(torch.bfloat16), cache, table, [900], 64, True, scale=0.25)
 
 
+def test_attention_zero_queries_and_zero_pages():
+    """Rows of q that are zero see every key alike; a head whose K or V is zero
+    (whose pages then have the least scale there is) beside hidden tokens."""
+    for Nq in (1, 5, 40):
+        cache, table = attention_case(1, 3, 64, 16, [90], 14)
+        x = torch.randn(1, 3, 90, 64, generator=torch.Generator().manual_seed(3))
+        k, v = x.clone(), x.flip(2).contiguous()
+        k[:, 0], v[:, 1], v[:, 2, 32:64] = 0, 0, 0
+        F.cache_append(k.cuda(), v.cuda(), *cache, table.cuda(), i32([0]))
+        assert float(cache[2][int(table[0, 0]), 0]) == S.SCALE_MIN
+        q = torch.randn(1, 6, Nq, 64, generator=torch.Generator().manual_seed(7))
+        q[:, ::2] = 0
+        check_attention(q.to(torch.bfloat16), cache, table, [90], 16, True)
+
+
+@pytest.mark.parametrize("Nq", [1, 30])
+def test_attention_one_long_sequence_among_many(Nq):
+    """More sequences than lanes; nearly all of the work in one of them, so that
+    its units are cut into many pieces while the others have one or none."""
+    B = 70
+    lens = [[0, 1, 5, 17, 40][b % 5] for b in range(B)]
+    lens[41] = 9000
+    cache, table = attention_case(B, 1, 64, 64, lens, 15)
+    q = torch.randn(B, 2, Nq, 64, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
+    check_attention(q, cache, table, lens, 64, True)
+
+
+def test_cache_beyond_four_gigabytes():
+    """Pages whose codes lie past 2^32 bytes: append, attention of few and of
+    many rows, read."""
+    H, page, d = 8, 128, 256
+    num_pages = 2 ** 32 // (H * page * d) + 6
+    if torch.cuda.mem_get_info()[0] < 4 * num_pages * H * page * d:
+        pytest.skip("not enough device memory")
+    cache = [torch.empty(num_pages, H, page, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.ones(num_pages, H, device="cuda") for _ in range(2)]
+    table = torch.tensor([[num_pages - 1, 0, num_pages - 3]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(16)
+    x = torch.randn(2, 1, H, 300, d, generator=g)
+    F.cache_append(x[0].cuda(), x[1].cuda(), *cache, table.cuda(), i32([0]))
+    small = [c[table[0].long()].contiguous() for c in cache]     # the three pages alone
+    ref = np_cache(new_cache(3, H, page, d))
+    for i in (0, 1):
+        S.cache_append(f64(x[i]), ref[i], ref[i + 2], [[0, 1, 2]], [0], None, page)
+        assert np.array_equal(f64(small[i + 2]), ref[i + 2])
+        for p in range(3):
+            n = min(page, 300 - page * p)
+            assert np.array_equal(small[i][p, :, :n].cpu().numpy(), ref[i][p, :, :n])
+    first = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    for Nq in (1, 100):
+        q = torch.randn(1, H, Nq, d, generator=g).to(torch.bfloat16).cuda()
+        a = F.forward_cache(q, *cache, table.cuda(), i32([300]))
+        b = F.forward_cache(q, *small, first, i32([300]))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = F.cache_read(*cache, table.cuda(), i32([300]), 300), F.cache_read(*small, first, i32([300]), 300)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert F.fa_device_status() == F.FA_OK
+
+
 def test_attention_shared_and_repeated_pages():
     """Two sequences that share a prefix's pages, and one whose table names a page twice."""
     cache, table = attention_case(3, 2, 64, 16, [80, 80, 80], 9)
@@ -407,7 +466,7 @@ def test_attention_leaves_out_what_is_out_of_range(Nq):
     compare_attention(o, lse, q, cache, table, cut, 16, True, 128 ** -0.5)
 
 
-@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("Nq", [1, 12, 40])
 def test_attention_nan_reaches_only_the_rows_that_see_it(Nq):
     """A NaN code of V in token t makes column c of the rows that see t NaN and no other value."""
     cache, table = attention_case(1, 1, 128, 32, [200], 12)
