@@ -10,6 +10,7 @@ the library's CUDA kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 FA_OK = 0
@@ -26,7 +27,8 @@ FA_ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libfa.so")
 _lib = None
-_torch = None   # the torch module, once a wrapper of the serving operators has run
+# torch and what the serving operators' wrappers use of it, once one has run
+_torch = _F32 = _BF16 = _I32 = _F8 = _get_device = _get_stream = None
 
 EXPORTS = ("fa_fwd", "fa_fwd_pair", "fa_fwd_fp8", "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_splitkv",
            "fa_fwd_splitkv_num_splits",
@@ -329,12 +331,17 @@ def _workspace(where, workspace, B, Hq, Nq, d, device):
 
 
 # The serving operators' wrappers are called once a layer and token, so they
-# keep their own time down: torch is imported once, the context switch and the
-# stream object are skipped where the device is current already.
+# keep their own time down: torch's names are looked up once, the context switch
+# and the stream object are skipped where the device is current already.
 def _t():
-    global _torch
+    global _torch, _F32, _BF16, _I32, _F8, _get_device, _get_stream
     if _torch is None:
         import torch
+        _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+        _F8 = (torch.float8_e4m3fn, torch.uint8)
+        _get_device = torch.cuda.current_device
+        _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch
     return _torch
 
@@ -342,13 +349,12 @@ def _t():
 def _call(fn, name, dev, *args):
     """fn(*args, stream) on CUDA device number `dev` and its current stream;
     raises FaError."""
-    torch = _torch
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if _get_device() == dev:
+        st = fn(*args, _get_stream(dev))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
+        with _torch.cuda.device(dev):
+            st = fn(*args, _get_stream(dev))
+    if st:
         raise FaError(st, name)
 
 
@@ -531,7 +537,7 @@ def rope_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=
 def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
     torch = _t()
     shape, dtype = q.shape, q.dtype
-    if len(shape) != 4 or (dtype is not torch.bfloat16 and dtype is not torch.float32):
+    if len(shape) != 4 or (dtype is not _BF16 and dtype is not _F32):
         raise ValueError(f"{where}: q must be [B, Hq, N, d], bfloat16 or float32")
     B, Hq, N, d = shape
     Hkv = 0
@@ -542,7 +548,7 @@ def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
         Hkv = ks[1]
     ps = positions.shape
     per_batch = len(ps) == 2
-    if positions.dtype is not torch.int32 or ps != ((B, N) if per_batch else (N,)):
+    if positions.dtype is not _I32 or ps != ((B, N) if per_batch else (N,)):
         raise ValueError(f"{where}: positions must be int32 [B, N] or [N]")
     fs = freqs.shape
     if len(fs) != 1 or freqs.dtype is not torch.float64:
@@ -559,7 +565,7 @@ def _rope(where, q, k, positions, freqs, mscale, interleaved, out, name):
     if out is None:   # contiguous, as q and k are
         qo = torch.empty_like(q)
         ko = None if k is None else torch.empty_like(k)
-    if dtype is torch.float32:
+    if dtype is _F32:
         name += "_f32"
     _call(getattr(_lib or lib(), name), name, dev, q.data_ptr(), 0 if k is None else k.data_ptr(),
           qo.data_ptr(), 0 if k is None else ko.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
@@ -587,22 +593,19 @@ def _check_cache(where, ref, k_cache, v_cache, k_scale, v_scale, block_table, B,
     """The cache's tensors against B, Hkv, d; lens (called `name`): int32 [B];
     more: tensors whose place alone is checked.  Returns (page, num_pages,
     max_pages, device number)."""
-    torch = _torch
-    f8 = (torch.float8_e4m3fn, torch.uint8)
     shape = k_cache.shape
     if (len(shape) != 4 or shape[1] != Hkv or shape[3] != d or v_cache.shape != shape
-            or k_cache.dtype not in f8 or v_cache.dtype not in f8):
+            or k_cache.dtype not in _F8 or v_cache.dtype not in _F8):
         raise ValueError(f"{where}: k_cache and v_cache must be E4M3 [num_pages, Hkv, page, d]")
     num_pages, _, page, _ = shape
     shape = (num_pages, Hkv)
-    f32, i32 = torch.float32, torch.int32
-    if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype is not f32
-            or v_scale.dtype is not f32):
+    if (k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype is not _F32
+            or v_scale.dtype is not _F32):
         raise ValueError(f"{where}: k_scale and v_scale must be float32 [num_pages, Hkv]")
     shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B or block_table.dtype is not i32:
+    if len(shape) != 2 or shape[0] != B or block_table.dtype is not _I32:
         raise ValueError(f"{where}: block_table must be int32 [B, max_pages]")
-    if lens is None or lens.shape != (B,) or lens.dtype is not i32:
+    if lens is None or lens.shape != (B,) or lens.dtype is not _I32:
         raise ValueError(f"{where}: {name} must be int32 [B]")
     dev = _check_place(where, ref, (k_cache, v_cache, k_scale, v_scale, block_table, lens) + more)
     return page, num_pages, shape[1], dev
@@ -614,21 +617,21 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, c
     power-of-two scale per page and head (fa_cache_append).  count: int32 [B]
     tokens of each sequence that count (None: all T).  The cache tensors are
     updated in place."""
-    torch = _t()
+    _t()
     shape, dtype = k.shape, k.dtype
     if (len(shape) != 4 or v.shape != shape or v.dtype is not dtype
-            or (dtype is not torch.bfloat16 and dtype is not torch.float32)):
+            or (dtype is not _BF16 and dtype is not _F32)):
         raise ValueError("cache_append: k and v must both be [B, Hkv, T, d], bfloat16 or float32")
     B, Hkv, T, d = shape
     more = (v,)
     if count is not None:
-        if count.shape != (B,) or count.dtype is not torch.int32:
+        if count.shape != (B,) or count.dtype is not _I32:
             raise ValueError("cache_append: count must be int32 [B]")
         more = (v, count)
     page, num_pages, max_pages, dev = _check_cache("cache_append", k, k_cache, v_cache, k_scale,
                                                    v_scale, block_table, B, Hkv, d, "start", start,
                                                    *more)
-    name = "fa_cache_append_f32" if dtype is torch.float32 else "fa_cache_append"
+    name = "fa_cache_append_f32" if dtype is _F32 else "fa_cache_append"
     _call(getattr(_lib or lib(), name), name, dev, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
           start.data_ptr(), 0 if count is None else count.data_ptr(), B, Hkv, T, d, page,
@@ -651,13 +654,18 @@ def cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, N, dtype=N
     page, num_pages, max_pages, dev = _check_cache("cache_read", k_cache, k_cache, v_cache,
                                                    k_scale, v_scale, block_table, B, Hkv, d,
                                                    "lens", lens)
-    k = torch.empty((B, Hkv, N, d), device=k_cache.device, dtype=dtype)
+    k = torch.empty(B, Hkv, N, d, device=k_cache.device, dtype=dtype)
     v = torch.empty_like(k)
     name = "fa_cache_read_f32" if dtype is torch.float32 else "fa_cache_read"
     _call(getattr(_lib or lib(), name), name, dev, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
           k.data_ptr(), v.data_ptr(), B, Hkv, N, d, page, num_pages, max_pages)
     return k, v
+
+
+@functools.lru_cache(maxsize=256)   # a step's layers ask for the same sizes
+def _fwd_cache_bytes(*sizes):
+    return lib().fa_fwd_cache_workspace_size(*sizes)
 
 
 def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scale=None, causal=True,
@@ -668,7 +676,7 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     Nq of those tokens.  A query that sees no key gets O = 0, L = -inf."""
     torch = _t()
     shape = q.shape
-    if len(shape) != 4 or q.dtype is not torch.bfloat16 or k_cache.dim() != 4:
+    if len(shape) != 4 or q.dtype is not _BF16 or k_cache.dim() != 4:
         raise ValueError("forward_cache: q must be bfloat16 [B, Hq, Nq, d], k_cache "
                          "[num_pages, Hkv, page, d]")
     B, Hq, Nq, d = shape
@@ -677,7 +685,7 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
                                                    v_scale, block_table, B, Hkv, d, "lens", lens)
     L = _lib or lib()
     place = q.device
-    need = L.fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, max_pages)
+    need = _fwd_cache_bytes(B, Hq, Hkv, Nq, d, page, max_pages)
     if workspace is None:
         workspace = torch.empty(need, device=place, dtype=torch.uint8)
     elif (not workspace.is_cuda or not workspace.is_contiguous()
@@ -688,7 +696,7 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
         raise ValueError(f"forward_cache: workspace must be on q's device ({place}); "
                          f"got {workspace.device}")
     o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Nq), device=place, dtype=torch.float32)
+    lse = torch.empty(B, Hq, Nq, device=place, dtype=_F32)
     _call(L.fa_fwd_cache, "fa_fwd_cache", dev, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
           lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
