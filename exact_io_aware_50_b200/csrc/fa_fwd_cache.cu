@@ -41,13 +41,17 @@ constexpr int kSub = 16;                        // tokens of a subtile (one page
 constexpr int kGranule = kWarps * kSub;
 constexpr int kStage = 8 * 1024, kStages = 3;   // a warp's ring
 constexpr int kRing = kStage * kStages;
-using RowLine = Line<16, kGranule, false>;
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
 constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 
 template <int D>
 struct RowCfg {
   static constexpr int ROWS = 16;
+  // A unit's start counts as four granules.  Measured, us a call in a graph
+  // with 0 / 2 / 4 / 6: one sequence of 16384 tokens (Hq 32, Hkv 8, d 128) 16.3 /
+  // 15.2 / 14.1 / 14.1; 32 ragged ones to 16384 104.7 / 103.0 / 100.4 / 100.5;
+  // d = 256, B 8, four drafted tokens 32.3 / 29.9 / 28.5 / 28.2.
+  using L = Line<ROWS, kGranule, false, 4>;
   static constexpr int CH = D / 16;             // 16-byte chunks of a token
   static constexpr int NS = 256 / D;            // subtiles of a step
   static constexpr int TILE = kSub * D;         // K or V codes of a subtile
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
   const int warp = warp_id_uniform(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   launch_dependents();   // the merge kernel's CTAs may take their places
-  Run<RowLine> run;
+  Run<typename C::L> run;
   if (!run.start(p) || !run.next(p)) return;
 
   const uint32_t sbase = smem_u32(smem), ring = sbase + warp * kRing;
@@ -563,7 +567,7 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   if (!allow_smem(kern, C::SMEM, &allowed)) return 5;
   kern<<<x.ctas, kWarps * 32, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
-  return launch_fwd_cache_merge<D, RowLine>(p, a.stream);
+  return launch_fwd_cache_merge<D, typename C::L>(p, a.stream);
 }
 
 // Up to three tiles of 16 rows (two at d = 256) go to the kernel of this file,
@@ -573,11 +577,14 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
 // 96.7 / 91.6; d = 128, 40 rows 74.5 / 80.6, 64 rows 95.8 / 85.6; d = 256, 32 rows
 // 96.6 / 116, 40 rows 126 / 121.
 bool few_rows(const CacheArgs &a) {
-  return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 256 ? 2 : 3) * RowLine::ROWS;
+  return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 256 ? 2 : 3) * 16;
 }
 
 FwdCachePlan plan_of(const CacheArgs &a) {
-  return few_rows(a) ? fwd_cache_plan(a, RowLine::ROWS, kGranule, kMaxCtas) : fwd_cache_tile_plan(a);
+  if (!few_rows(a)) return fwd_cache_tile_plan(a);
+  return a.d == 64    ? fwd_cache_plan<RowCfg<64>::L>(a, kMaxCtas)
+         : a.d == 128 ? fwd_cache_plan<RowCfg<128>::L>(a, kMaxCtas)
+                      : fwd_cache_plan<RowCfg<256>::L>(a, kMaxCtas);
 }
 
 }  // namespace

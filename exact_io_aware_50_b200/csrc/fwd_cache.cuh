@@ -43,15 +43,18 @@ __device__ __forceinline__ int warp_sum(int v) {
 // The work: a unit is (sequence, key/value head, tile of ROWS query rows), its
 // tokens in granules of GRANULE.  The granules of all units stand in one line
 // (sequences in order, each its heads, each its tiles; fewer than 2^31: the
-// launcher checks), which is cut into p.ctas even runs.
+// launcher checks), which is cut into p.ctas even runs.  A unit that begins in a
+// run costs its CTA some time before and after its granules: each unit stands in
+// the line with START empty granules in front, so that a CTA that ends one unit
+// and begins another gets less of them.
 //
 // QMAJOR: row r of a head is query r / g of its group's head r % g, so a tile
 // holds consecutive queries and, causal, sees no further than its last one;
 // else row r is query r % Nq of head r / Nq, the order of memory, and every tile
 // of a sequence has the same granules.
-template <int ROWS_, int GRANULE_, bool QMAJOR_>
+template <int ROWS_, int GRANULE_, bool QMAJOR_, int START_>
 struct Line {
-  static constexpr int ROWS = ROWS_, GRANULE = GRANULE_;
+  static constexpr int ROWS = ROWS_, GRANULE = GRANULE_, START = START_;
   static constexpr bool QMAJOR = QMAJOR_;
 
   static __device__ __forceinline__ int len(const FwdCacheParams &p, int b) {
@@ -66,14 +69,19 @@ struct Line {
     }
     return (seen + GRANULE - 1) / GRANULE;
   }
-  // granules of one head: all its tiles
+  // the unit's part of the line
+  static __device__ __forceinline__ int span(const FwdCacheParams &p, int len, int tile) {
+    const int n = granules(p, len, tile);
+    return n ? n + START : 0;
+  }
+  // one head's: all its tiles
   static __device__ __forceinline__ int head(const FwdCacheParams &p, int len) {
-    if constexpr (!QMAJOR) return granules(p, len, 0) * p.tiles;
+    if constexpr (!QMAJOR) return span(p, len, 0) * p.tiles;
     int sum = 0;
-    for (int t = 0; t < p.tiles; ++t) sum += granules(p, len, t);
+    for (int t = 0; t < p.tiles; ++t) sum += span(p, len, t);
     return sum;
   }
-  // The granules of one head of all sequences, and of those before sequence
+  // The parts of one head of all sequences, and of those before sequence
   // b; every warp forms them for itself.
   static __device__ __forceinline__ void sums(const FwdCacheParams &p, int b, int *total, int *before) {
     int all = 0, pre = 0;
@@ -150,30 +158,34 @@ struct Run {
     return pos < end;
   }
   __device__ __forceinline__ bool next(const FwdCacheParams &p) {
-    if (pos >= end) return false;
-    len = L::len(p, b);
-    int n = L::head(p, len);
-    while (pos - b_first >= n * p.Hkv) {   // on to the next sequence with tokens
-      b_first += n * p.Hkv;
-      ++b;
+    while (pos < end) {
       len = L::len(p, b);
-      n = L::head(p, len);
+      int n = L::head(p, len);
+      while (pos - b_first >= n * p.Hkv) {   // on to the next sequence with tokens
+        b_first += n * p.Hkv;
+        ++b;
+        len = L::len(p, b);
+        n = L::head(p, len);
+      }
+      h = (pos - b_first) / n;
+      int at = pos - b_first - h * n, tile, span;   // place within the unit
+      if constexpr (L::QMAJOR) {
+        for (tile = 0; at >= (span = L::span(p, len, tile)); ++tile) at -= span;
+      } else {
+        span = L::span(p, len, 0);
+        tile = at / span;
+        at -= tile * span;
+      }
+      const int to = min(span, at + (end - pos));
+      pos += to - at;
+      ng = span - L::START;
+      g0 = max(0, at - L::START);
+      g1 = to - L::START;
+      r0 = tile * L::ROWS;
+      stop = min(len, g1 * L::GRANULE);
+      if (g0 < g1) return true;   // else the run ended before the unit's first granule
     }
-    h = (pos - b_first) / n;
-    int rest = pos - b_first - h * n, tile;
-    if constexpr (L::QMAJOR) {
-      for (tile = 0; rest >= (ng = L::granules(p, len, tile)); ++tile) rest -= ng;
-    } else {
-      ng = L::granules(p, len, 0);
-      tile = rest / ng;
-      rest -= tile * ng;
-    }
-    g0 = rest;
-    g1 = min(ng, g0 + (end - pos));
-    pos += g1 - g0;
-    r0 = tile * L::ROWS;
-    stop = min(len, g1 * L::GRANULE);
-    return true;
+    return false;
   }
   // first row of the piece's partial, -1 where the piece is the whole unit: a
   // run has at most one piece that starts inside its unit (slot 0) and one that
@@ -220,9 +232,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const
   const int per = max((total * p.Hkv + p.ctas - 1) / p.ctas, 1);
   first = first * p.Hkv + h * L::head(p, len);
   if constexpr (L::QMAJOR)
-    for (int t = 0; t < tile; ++t) first += L::granules(p, len, t);
+    for (int t = 0; t < tile; ++t) first += L::span(p, len, t);
   else
-    first += tile * ng;
+    first += tile * L::span(p, len, 0);
+  first += L::START;   // the unit's first granule
   const int c0 = first / per, n = ng == 0 ? 0 : (first + ng - 1) / per - c0 + 1;
   // every CTA waits, so that what follows in the stream finds o and lse whole
   wait_for_primary();
@@ -332,20 +345,21 @@ int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
 
-// What the host knows of the work of tiles of `rows` rows and granules of
-// `granule` tokens: CTAs (fewer than `most_ctas` when the block table has room
-// for fewer granules), rows of a partial.
+// What the host knows of the work of a line: CTAs (fewer than `most_ctas` when
+// the block table has room for fewer granules), rows of a partial.
 struct FwdCachePlan {
-  double R, most;   // most: granules when every sequence fills its table
+  double R, most;   // most: the line's length when every sequence fills its table
   long long tiles;
   int prows, ctas;
 };
-inline FwdCachePlan fwd_cache_plan(const CacheArgs &a, int rows, int granule, int most_ctas) {
+template <class L>
+FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas) {
   FwdCachePlan x;
   x.R = (double)(a.Hq / a.Hkv) * a.Nq;
-  x.prows = x.R < rows ? (int)x.R : rows;
-  x.tiles = (long long)((x.R + rows - 1) / rows);
-  x.most = (double)a.B * a.Hkv * x.tiles * (((long long)a.max_pages * a.page + granule - 1) / granule);
+  x.prows = x.R < L::ROWS ? (int)x.R : L::ROWS;
+  x.tiles = (long long)((x.R + L::ROWS - 1) / L::ROWS);
+  x.most = (double)a.B * a.Hkv * x.tiles *
+           (((long long)a.max_pages * a.page + L::GRANULE - 1) / L::GRANULE + L::START);
   x.ctas = x.most < most_ctas ? (int)x.most : most_ctas;
   return x;
 }
