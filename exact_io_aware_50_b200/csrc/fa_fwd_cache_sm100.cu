@@ -39,7 +39,7 @@ template <int D_, int NT_>
 struct TileCfg {
   static constexpr int D = D_, NT = NT_;
   // A unit's start counts as five granules.  Measured, us a call in a graph with
-  // 0 / 2 / 3 / 5: 512 queries over 16384 tokens, causal, Hq 32, Hkv 8, d 128:
+  // 0 / 2 / 3 / 5: 512 queries over 16384 tokens, causal, Hq 8, Hkv 8, d 128:
   // 71.4 / 66.6 / 65.7 / 65.2.
   using L = Line<NT * BM, BN, true, 5>;
   static constexpr int SOFT = 4 * NT;                 // softmax warps
@@ -158,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{p.err, abort_flag, kWaitLimitNs};
-  const int group = p.Hq / p.Hkv;
 
   // Blocks of the run are counted by g, pieces by u: barrier phases.
   if (warp >= C::SOFT && warp < kMmaWarp) {
@@ -254,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       float2 sc = scale_of(row0);
 
       // tokens that every row of the piece sees
-      const int lim_min = p.causal ? max(0, min(run.len, run.len - p.Nq + run.r0 / group + 1)) : run.len;
+      const int lim_min = p.causal ? max(0, min(run.len, run.len - p.Nq + run.r0 / p.g + 1)) : run.len;
 
       for (int j = 0; j <= n && ok; ++j) {
         // K runs a block ahead of V
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       if (x.blocks == 0) break;
       const int rr = x.r0 + t * BM + r;              // row of the head
       const bool live = rr < p.R;
-      const int i = (live ? rr : 0) / group, hq = x.h * group + (live ? rr : 0) - i * group;
+      const int i = (live ? rr : 0) / p.g, hq = x.h * p.g + (live ? rr : 0) - i * p.g;
       // tokens [0, lim) visible; the warp's least, for whole blocks
       const int lim = !live ? x.len : (p.causal ? max(0, min(x.len, x.len - p.Nq + i + 1)) : x.len);
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);

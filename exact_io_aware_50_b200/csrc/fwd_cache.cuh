@@ -27,12 +27,45 @@ struct FwdCacheParams {
   __nv_bfloat16 *o;
   float *lse;
   float *o_part, *l_part;   // [ctas][2][prows][D], [ctas][2][prows] (base 2)
-  int B, Hq, Hkv, Nq, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
+  int B, Hq, Hkv, Nq, g, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
   int page_log2, num_pages, max_pages;
   int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
   float scale_log2;
+  unsigned long long g_inv;   // ceil(2^64 / g), 0 for g = 1
   unsigned *err;
 };
+
+// x / p.g, x >= 0: below 2^32 a product, which is exact (the excess of g_inv g over
+// 2^64 is less than g < 2^31, so x times it stays below 2^64).
+__device__ __forceinline__ long long div_g(long long x, int g, unsigned long long g_inv) {
+  if (x >> 32) return x / g;
+  return g_inv ? (long long)__umul64hi((unsigned long long)x, g_inv) : x;
+}
+
+// The parts of the line (below) of the tiles before `tile`, causal, for tiles of
+// 128 NT rows and granules of 128 tokens: tile t but the last sees floor((NT t + c)
+// / g) granules where that is positive, with c = floor(((len - Nq + 128) g + 128 NT
+// - 1) / 128), so the sum has a closed form.  With t0 the first tile that sees a
+// token, n = tile - t0 and NT t0 + c = base g + rest it is
+//     n (base + START) + sum_{i < n} floor((NT i + rest) / g),
+// whose last sum counts, for k = 1 .. K = floor((NT (n - 1) + rest) / g), the i with
+// NT i + rest >= k g: K n - sum_k ceil((k g - rest) / NT).  (A tile by tile sum took
+// 3.4 ms of a square causal call of 8192 queries, Hq 32, Hkv 8, d 128: all else 0.8.)
+template <int NT, int START>
+__device__ __forceinline__ int parts_before(int tile, int len, int Nq, int g, unsigned long long g_inv) {
+  static_assert(NT == 1 || NT == 2, "the odd terms");
+  long long c = ((long long)(len - Nq + 128) * g + 128 * NT - 1) >> 7, t0 = 0;
+  if (c < g) {
+    t0 = (g - c + NT - 1) / NT;
+    c += NT * t0;
+  }
+  if (tile <= t0) return 0;
+  const long long base = div_g(c, g, g_inv), rest = c - base * g, n = tile - t0;
+  const long long K = div_g(NT * (n - 1) + rest, g, g_inv);
+  long long up = g * (K * (K + 1) / 2) - K * rest;   // sum of k g - rest
+  if (NT == 2) up = (up + (g & 1 ? (K + 1 - (rest & 1)) / 2 : K * (rest & 1))) / 2;   // the odd ones round up
+  return (int)(n * (base + START) + K * n - up);
+}
 
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
@@ -64,7 +97,7 @@ struct Line {
   static __device__ __forceinline__ int granules(const FwdCacheParams &p, int len, int tile) {
     int seen = len;
     if (QMAJOR && p.causal) {
-      const int last = (min(p.R, (tile + 1) * ROWS) - 1) / (p.Hq / p.Hkv);
+      const int last = (int)div_g((tile + 1 < p.tiles ? (tile + 1) * ROWS : p.R) - 1, p.g, p.g_inv);
       seen = max(0, len - p.Nq + last + 1);
     }
     return (seen + GRANULE - 1) / GRANULE;
@@ -74,12 +107,36 @@ struct Line {
     const int n = granules(p, len, tile);
     return n ? n + START : 0;
   }
+  // the parts of the tiles before `tile` of one head
+  static __device__ __forceinline__ int before(const FwdCacheParams &p, int len, int tile) {
+    if constexpr (QMAJOR) {
+      static_assert(GRANULE == 128 && ROWS % 128 == 0, "parts_before");
+      if (p.causal && tile > 0) return parts_before<ROWS / 128, START>(tile, len, p.Nq, p.g, p.g_inv);
+    }
+    return tile * span(p, len, 0);
+  }
   // one head's: all its tiles
   static __device__ __forceinline__ int head(const FwdCacheParams &p, int len) {
-    if constexpr (!QMAJOR) return span(p, len, 0) * p.tiles;
-    int sum = 0;
-    for (int t = 0; t < p.tiles; ++t) sum += span(p, len, t);
-    return sum;
+    return before(p, len, p.tiles - 1) + span(p, len, p.tiles - 1);
+  }
+  // The tile whose part holds place `at` of a head's, at < head(len), and the
+  // place within it; a warp looks together.
+  static __device__ __forceinline__ int tile_at(const FwdCacheParams &p, int len, int &at) {
+    int lo = 0;
+    if (!QMAJOR || !p.causal) {
+      lo = at / span(p, len, 0);
+    } else {
+      const int lane = threadIdx.x & 31;
+      for (int n = p.tiles; n > 1;) {   // in [lo, lo + n)
+        const int step = (n + 31) / 32;
+        const bool under = lane * step < n && before(p, len, lo + lane * step) <= at;
+        const int k = __popc(__ballot_sync(0xffffffffu, under)) - 1;   // lane 0 is: before(lo) <= at
+        lo += k * step;
+        n = min(step, n - k * step);
+      }
+    }
+    at -= before(p, len, lo);
+    return lo;
   }
   // The parts of one head of all sequences, and of those before sequence
   // b; every warp forms them for itself.
@@ -168,14 +225,8 @@ struct Run {
         n = L::head(p, len);
       }
       h = (pos - b_first) / n;
-      int at = pos - b_first - h * n, tile, span;   // place within the unit
-      if constexpr (L::QMAJOR) {
-        for (tile = 0; at >= (span = L::span(p, len, tile)); ++tile) at -= span;
-      } else {
-        span = L::span(p, len, 0);
-        tile = at / span;
-        at -= tile * span;
-      }
+      int at = pos - b_first - h * n;   // place within the head, then the unit
+      const int tile = L::tile_at(p, len, at), span = L::span(p, len, tile);
       const int to = min(span, at + (end - pos));
       pos += to - at;
       ng = span - L::START;
@@ -211,115 +262,133 @@ __device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
 
 // Joins the pieces of the units that several CTAs covered: W warps of a
 // CTA of kMergeWarps take one query row.  W is kMergeWarps where a unit has many
-// pieces, 1 where it has few (a warp has eight in flight).  Rows of tiles that see
+// pieces, 1 where it has few.  Rows of tiles that see
 // no token become O = 0, L = -inf.
 constexpr int kMergeWarps = 8;
+constexpr int kMergeCtas = 148 * 16;   // of warps a row, at most
+
+// Pieces in flight.  Units of 128 rows and more have two or three pieces, and rows
+// enough that more warps matter more: four (512 queries over 16384 tokens, Hq 8,
+// Hkv 8, d 128: 67.2 us a call with eight, 66.0 with four; a square causal call of
+// 2048 queries, Hq 32: 115.7 and 112.6).
+template <class L, int W>
+constexpr int merge_ahead() { return W == 1 && L::QMAJOR ? 4 : 8; }
 
 template <int D, class L, int W>
-__global__ void __launch_bounds__(kMergeWarps * 32) fwd_cache_merge_kernel(const FwdCacheParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1 : D == 256 ? 3 : 4) fwd_cache_merge_kernel(const FwdCacheParams p, int each) {
   __shared__ float s_o[W > 1 ? kMergeWarps : 1][D], s_w[kMaxCtas];
   const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
-  const int row = W > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const bool exists = row < p.B * p.Hq * p.Nq;
-  const int b = exists ? row / (p.Hq * p.Nq) : 0, hr = exists ? row - b * p.Hq * p.Nq : 0;   // row within the sequence
-  const int h = hr / p.R;
-  int r = hr - h * p.R;   // row of the head, in the order of memory
-  if constexpr (L::QMAJOR) r = r % p.Nq * (p.Hq / p.Hkv) + r / p.Nq;
-  const int tile = r / L::ROWS, rr = r - tile * L::ROWS;
-  const int len = L::len(p, b), ng = L::granules(p, len, tile);
-  int total, first;
-  L::sums(p, b, &total, &first);
-  const int per = max((total * p.Hkv + p.ctas - 1) / p.ctas, 1);
-  first = first * p.Hkv + h * L::head(p, len);
-  if constexpr (L::QMAJOR)
-    for (int t = 0; t < tile; ++t) first += L::span(p, len, t);
-  else
-    first += tile * L::span(p, len, 0);
-  first += L::START;   // the unit's first granule
-  const int c0 = first / per, n = ng == 0 ? 0 : (first + ng - 1) / per - c0 + 1;
+  const int rows = p.B * p.Hq * p.Nq;   // < 2^31: the launcher checks
+  const int who = W > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int row0 = (int)min((long long)rows, (long long)who * each), row1 = min(rows - row0, each) + row0;
+  int unit_b = -1, unit_h, unit_tile, c0 = 0, n = 0, rr;   // the last row's unit, its first CTA and pieces
+  // row -> its unit (looked for where it is another than the last row's) and rr, the row of the tile
+  auto look = [&](int row) {
+    const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
+    const int h = hr / p.R;
+    int r = hr - h * p.R;   // row of the head, in the order of memory
+    if constexpr (L::QMAJOR) r = r % p.Nq * p.g + r / p.Nq;
+    const int tile = r / L::ROWS;
+    rr = r - tile * L::ROWS;
+    if (b == unit_b && h == unit_h && tile == unit_tile) return;
+    unit_b = b; unit_h = h; unit_tile = tile;
+    const int len = L::len(p, b), ng = L::granules(p, len, tile);
+    int total, first;
+    L::sums(p, b, &total, &first);
+    const int per = max((total * p.Hkv + p.ctas - 1) / p.ctas, 1);
+    // the unit's first granule
+    first = first * p.Hkv + h * L::head(p, len) + L::before(p, len, tile) + L::START;
+    c0 = first / per;
+    n = ng == 0 ? 0 : (first + ng - 1) / per - c0 + 1;
+  };
+  if (row0 < row1) look(row0);
   // every CTA waits, so that what follows in the stream finds o and lse whole
   wait_for_primary();
-  if (n == 1 || !exists) return;
-  // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
-  auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
-  constexpr int PER = D / 32, AHEAD = 8;
-  const float *src = p.o_part + lane * PER;
-  // warp w adds pieces w, w + W, ...: the first loads go out before the weights are known
-  float v[AHEAD][PER];
-#pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-    if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
-  // lane i looks at pieces i, i + 32, ...
-  const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
-  float top = mine;
-  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
-  float sum = own;
-  if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
-  for (int i = lane + 32; i < n; i += 32) {
-    const float x = p.l_part[at(i)];
-    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-    sum += w;
-    if (W > 1 && i % W == warp) s_w[i] = w;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  __syncwarp();
-  float acc[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
 #pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += AHEAD * W) {
-    if (i0 != warp) {
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (i0 + W * k < n) load_floats<PER>(src + at(i0 + W * k) * D, v[k]);
-    }
+  for (int row = row0; row < row1; ++row) {
+    if (row > row0) look(row);
+    if (n == 1) continue;
+    // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
+    auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
+    constexpr int PER = D / 32, AHEAD = merge_ahead<L, W>();
+    const float *src = p.o_part + lane * PER;
+    // warp w adds pieces w, w + W, ...: the first loads go out before the weights are known
+    float v[AHEAD][PER];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
-      if (i0 + W * k < n) {
-        const int i = i0 + W * k;
-        float w;
-        if (W > 1) {
-          w = s_w[i];
-        } else {
-          w = __shfl_sync(0xffffffffu, own, i & 31);
-          if (i >= 32) {   // more pieces than lanes: the weight again
-            const float x = p.l_part[at(i)];
-            w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-          }
-        }
+      if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
+    // lane i looks at pieces i, i + 32, ...
+    const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
+    float top = mine;
+    for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-      }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] *= inv;
-  __nv_bfloat16 *dst = p.o + (long long)row * D;
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
-    __syncthreads();
-    if (threadIdx.x < D / 2) {
-      float x = 0.f, y = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        x += s_o[w][2 * threadIdx.x];
-        y += s_o[w][2 * threadIdx.x + 1];
-      }
-      reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
+    float sum = own;
+    if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
+    for (int i = lane + 32; i < n; i += 32) {
+      const float x = p.l_part[at(i)];
+      const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+      sum += w;
+      if (W > 1 && i % W == warp) s_w[i] = w;
     }
-  } else {
 #pragma unroll
-    for (int e = 0; e < PER; e += 2)
-      reinterpret_cast<uint32_t *>(dst)[(lane * PER + e) / 2] = pack_bf16x2(acc[e], acc[e + 1]);
-  }
-  if (lane == 0 && warp == 0) {
-    p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-    if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncwarp();
+    float acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int i0 = warp; i0 < n; i0 += AHEAD * W) {
+      if (i0 != warp) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (i0 + W * k < n) load_floats<PER>(src + at(i0 + W * k) * D, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (i0 + W * k < n) {
+          const int i = i0 + W * k;
+          float w;
+          if (W > 1) {
+            w = s_w[i];
+          } else {
+            w = __shfl_sync(0xffffffffu, own, i & 31);
+            if (i >= 32) {   // more pieces than lanes: the weight again
+              const float x = p.l_part[at(i)];
+              w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= inv;
+    __nv_bfloat16 *dst = p.o + (long long)row * D;
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
+      __syncthreads();
+      if (threadIdx.x < D / 2) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          x += s_o[w][2 * threadIdx.x];
+          y += s_o[w][2 * threadIdx.x + 1];
+        }
+        reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e += 2)
+        reinterpret_cast<uint32_t *>(dst)[(lane * PER + e) / 2] = pack_bf16x2(acc[e], acc[e + 1]);
+    }
+    if (lane == 0 && warp == 0) {
+      p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      if (p.lens[unit_b] < 0) atomicOr(p.err, kErrPage);
+    }
   }
 }
 
@@ -334,13 +403,16 @@ int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(many ? (rows + kMergeWarps - 1) / kMergeWarps : rows), 1, 1);
+  // a warp takes neighbouring rows, which share their unit, rather than that more CTAs start
+  const long long each = many ? (rows + kMergeCtas * kMergeWarps - 1) / (kMergeCtas * kMergeWarps) : 1;
+  const long long warps = (rows + each - 1) / each;
+  cfg.gridDim = dim3((unsigned)(many ? (warps + kMergeWarps - 1) / kMergeWarps : rows), 1, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((many ? cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, 1>, p)
-            : cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, kMergeWarps>, p)) != cudaSuccess)
+  if ((many ? cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, 1>, p, (int)each)
+            : cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, kMergeWarps>, p, 1)) != cudaSuccess)
     return 5;
   return cudaGetLastError() == cudaSuccess ? 0 : 5;
 }
@@ -379,7 +451,8 @@ inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x
   p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
   p.o_part = (float *)a.ws;
   p.l_part = p.o_part + (size_t)x.ctas * 2 * x.prows * a.d;
-  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq;
+  p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq; p.g = a.Hq / a.Hkv;
+  p.g_inv = p.g == 1 ? 0 : ~0ull / p.g + 1;
   p.R = (int)x.R;
   p.tiles = (int)x.tiles;
   p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;

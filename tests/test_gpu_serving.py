@@ -351,6 +351,19 @@ def test_attention(c):
     check_attention(q, cache, table, lens, page, causal)
 
 
+@pytest.mark.parametrize("c", [   # many tiles of 128 or 256 rows a head
+    (2, 3, 1, 700, 64, 16, [700, 90], True),         # an odd group; most queries of the second see nothing
+    (1, 5, 1, 301, 128, 32, [1000], True),
+    (3, 8, 1, 220, 128, 64, [0, 221, 5], True),
+    (1, 7, 1, 120, 256, 128, [450], True),
+    (1, 6, 6, 517, 64, 64, [517], True),
+    (1, 4, 1, 1100, 128, 16, [1100], False),
+    (2, 64, 1, 400, 64, 32, [600, 433], True),       # 100 tiles; a warp of the merge takes several rows
+], ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+def test_many_tiles(c):
+    test_attention(c)
+
+
 @pytest.mark.parametrize("spread", [0.0, 4.0])
 def test_attention_any_scales(spread):
     """Scales that are no powers of two; pages and heads of very different size."""
