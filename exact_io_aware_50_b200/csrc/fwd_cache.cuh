@@ -397,8 +397,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1
 template <int D, class L>
 int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
   const long long rows = (long long)p.B * p.Hq * p.Nq, units = (long long)p.B * p.Hkv * p.tiles;
-  // a warp a row: about eight pieces a unit, or fewer, or rows enough to fill the GPU
-  const bool many = units * 8 >= p.ctas || rows > 148 * kMergeWarps;
+  // A warp a row: about eight pieces a unit, or fewer, or more rows than CTAs that
+  // run at once.  Measured, a call: Hq 16, Hkv 4, d 256, B 8, 2304 tokens, 4 queries
+  // (512 rows, 9 pieces) 20.2 us with a warp a row, 26.3 with eight; Hq 32, Hkv 8, d
+  // 128, B 4, 16384 tokens (128 rows, 9 pieces) 32.7 and 31.3.
+  const bool many = units * 8 >= p.ctas || rows > 2 * 148;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
