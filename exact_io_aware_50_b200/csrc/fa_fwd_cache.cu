@@ -55,9 +55,9 @@ struct RowCfg {
   static constexpr int CH = D / 16;             // 16-byte chunks of a token
   static constexpr int NS = 256 / D;            // subtiles of a step
   static constexpr int TILE = kSub * D;         // K or V codes of a subtile
-  // Steps of the next piece copied before the merge: the warp's O takes what
-  // is left of the ring.
-  static constexpr int AHEAD = D == 256 ? 1 : 2;
+  // Steps copied ahead of the one at hand.  Those of the next piece are under way
+  // when the warps' O are joined, in the stage that is left: JOIN columns at a time.
+  static constexpr int AHEAD = kStages - 1, JOIN = D < 128 ? D : 128;
   static constexpr int QROW = D * 2 + 16;       // q rows are padded: no two of eight in one bank group
   static constexpr int OFF_Q = kWarps * kRing;
   // d = 256: O's 128 registers leave no room for q's 64, which wait in shared
@@ -68,7 +68,7 @@ struct RowCfg {
   static constexpr int OFF_STAT = OFF_SCALE + kWarps * kStages * NS * 8; // [warp][ROWS]
   static constexpr int SMEM = OFF_STAT + kWarps * ROWS * 4;
   static_assert(2 * NS * TILE == kStage, "K and V codes of a step");
-  static_assert(ROWS * D * 4 <= (kStages - AHEAD) * kStage, "a warp's O fits beside the copies ahead");
+  static_assert(ROWS * JOIN * 4 <= kStage, "a warp's O fits beside the copies ahead");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
@@ -511,47 +511,55 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     if (more) begin(st);
 
     // ---- the four warps' results joined
-    // row r of a warp's O: what the copies ahead leave of its ring
+    // row r of a warp's O: the stage that the copies ahead leave
     auto o_at = [&](int w, int r) {
-      const int first = (st + C::AHEAD) % kStages, row = r * D * 4;
-      const int at = (first + row / kStage) % kStages * kStage + row % kStage;
-      return reinterpret_cast<float4 *>(smem + w * kRing + at);
+      return reinterpret_cast<float4 *>(smem + w * kRing + (st + C::AHEAD) % kStages * kStage + r * C::JOIN * 4);
     };
-    // o of columns 16 c + 4 t .. + 3 lies in two accumulators
+    float f[2];   // O / l_warp * 2^{L_warp - L}, O being in units of 2^{M - shift - m}
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
-      if (r >= rows) continue;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
-      // O / l_warp * 2^{L_warp - L}, O being in units of 2^{M - shift - m}
-      const float f = l[e] == 0.f ? 0.f
-                                  : fast_exp2(m_o[e] - kShift - m_s[e]) / l[e] *
-                                        (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
-      float4 *dst = o_at(warp, r) + t;
-#pragma unroll
-      for (int c = 0; c < C::CH; ++c)
-        dst[4 * c] = make_float4(o[2 * c][2 * e] * f, o[2 * c + 1][2 * e] * f, o[2 * c][2 * e + 1] * f,
-                                 o[2 * c + 1][2 * e + 1] * f);
+      f[e] = l[e] == 0.f ? 0.f
+                         : fast_exp2(m_o[e] - kShift - m_s[e]) / l[e] *
+                               (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-      const int r = i / (D / 4), c4 = i - r * (D / 4);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = o_at(w, r)[c4];
-        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    for (int half = 0; half < D / C::JOIN; ++half) {
+      if (half) __syncthreads();   // the columns before have been read
+      // o of columns 16 c + 4 t .. + 3 lies in two accumulators
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = g + 8 * e;
+        if (r >= rows) continue;
+        float4 *dst = o_at(warp, r) + t;
+#pragma unroll
+        for (int i = 0; i < C::JOIN / 16; ++i) {
+          const int c = half * (C::JOIN / 16) + i;
+          dst[4 * i] = make_float4(o[2 * c][2 * e] * f[e], o[2 * c + 1][2 * e] * f[e], o[2 * c][2 * e + 1] * f[e],
+                                   o[2 * c + 1][2 * e + 1] * f[e]);
+        }
       }
-      if (part < 0)
-        *reinterpret_cast<uint2 *>(p.o + (row0 + r) * D + 4 * c4) =
-            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      else
-        *reinterpret_cast<float4 *>(p.o_part + (long long)(part + r) * D + 4 * c4) = a;
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * (C::JOIN / 4); i += kWarps * 32) {
+        const int r = i / (C::JOIN / 4), c4 = i - r * (C::JOIN / 4), col = half * C::JOIN + 4 * c4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 x = o_at(w, r)[c4];
+          a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        }
+        if (part < 0)
+          *reinterpret_cast<uint2 *>(p.o + (row0 + r) * D + col) =
+              make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        else
+          *reinterpret_cast<float4 *>(p.o_part + (long long)(part + r) * D + col) = a;
+      }
     }
     if ((int)threadIdx.x < rows) {
       const int r = threadIdx.x;
