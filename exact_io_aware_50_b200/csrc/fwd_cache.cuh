@@ -260,10 +260,9 @@ __device__ __forceinline__ void load_floats(const float *src, float (&v)[PER]) {
   }
 }
 
-// Joins the pieces of the units that several CTAs covered: W warps of a
-// CTA of kMergeWarps take one query row.  W is kMergeWarps where a unit has many
-// pieces, 1 where it has few.  Rows of tiles that see
-// no token become O = 0, L = -inf.
+// Joins the pieces of the units that several CTAs covered: W warps of a CTA of
+// kMergeWarps take one query row.  W is kMergeWarps where a unit has many pieces, 1
+// where it has few.  Rows of tiles that see no token become O = 0, L = -inf.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeCtas = 148 * 16;   // of warps a row, at most
 
@@ -277,20 +276,27 @@ constexpr int merge_ahead() { return W == 1 && L::QMAJOR ? 4 : 8; }
 template <int D, class L, int W>
 __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1 : D == 256 ? 3 : 4) fwd_cache_merge_kernel(const FwdCacheParams p, int each) {
   __shared__ float s_o[W > 1 ? kMergeWarps : 1][D], s_w[kMaxCtas];
+  __shared__ int s_unit[5];
   const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
   const int rows = p.B * p.Hq * p.Nq;   // < 2^31: the launcher checks
-  const int who = W > 1 ? blockIdx.x : blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int row0 = (int)min((long long)rows, (long long)who * each), row1 = min(rows - row0, each) + row0;
-  int unit_b = -1, unit_h, unit_tile, c0 = 0, n = 0, rr;   // the last row's unit, its first CTA and pieces
-  // row -> its unit (looked for where it is another than the last row's) and rr, the row of the tile
-  auto look = [&](int row) {
-    const int b = row / (p.Hq * p.Nq), hr = row - b * p.Hq * p.Nq;   // row within the sequence
-    const int h = hr / p.R;
+  const long long cta0 = (long long)blockIdx.x * (W > 1 ? 1 : kMergeWarps * each);   // the CTA's first row
+  const int row0 = (int)min((long long)rows, cta0 + (W > 1 ? 0 : (int)(threadIdx.x >> 5) * each));
+  const int row1 = min(rows - row0, each) + row0;
+  int b = 0, h = 0, tile = 0, rr = 0;   // of a row: its unit, the row of the tile
+  int unit_b = -1, unit_h = 0, unit_tile = 0, c0 = 0, n = 0;   // a unit, its first CTA and pieces
+  auto place = [&](int row) {
+    b = row / (p.Hq * p.Nq);
+    const int hr = row - b * p.Hq * p.Nq;   // row within the sequence
+    h = hr / p.R;
     int r = hr - h * p.R;   // row of the head, in the order of memory
-    if constexpr (L::QMAJOR) r = r % p.Nq * p.g + r / p.Nq;
-    const int tile = r / L::ROWS;
+    if constexpr (L::QMAJOR) {
+      const int head = r / p.Nq;
+      r = (r - head * p.Nq) * p.g + head;
+    }
+    tile = r / L::ROWS;
     rr = r - tile * L::ROWS;
-    if (b == unit_b && h == unit_h && tile == unit_tile) return;
+  };
+  auto look = [&]() {
     unit_b = b; unit_h = h; unit_tile = tile;
     const int len = L::len(p, b), ng = L::granules(p, len, tile);
     int total, first;
@@ -301,12 +307,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1
     c0 = first / per;
     n = ng == 0 ? 0 : (first + ng - 1) / per - c0 + 1;
   };
-  if (row0 < row1) look(row0);
+  // With tiles of 128 rows and more most rows of the CTA are of one unit: one warp
+  // looks for it (512 queries over 16384 tokens, Hq 8, Hkv 8, d 128: 66.2 -> 63.8 us a
+  // call; with 16 rows a tile it costs 1 us, for the CTA's other units).
+  constexpr bool SHARE = L::QMAJOR && W == 1;
+  if (SHARE ? threadIdx.x < 32 : row0 < row1) {
+    place(SHARE ? (int)cta0 : row0);
+    look();
+    if (SHARE && lane == 0) {
+      s_unit[0] = unit_b; s_unit[1] = unit_h; s_unit[2] = unit_tile; s_unit[3] = c0; s_unit[4] = n;
+    }
+  }
   // every CTA waits, so that what follows in the stream finds o and lse whole
   wait_for_primary();
+  if (SHARE) {
+    __syncthreads();
+    unit_b = s_unit[0]; unit_h = s_unit[1]; unit_tile = s_unit[2]; c0 = s_unit[3]; n = s_unit[4];
+  }
 #pragma unroll 1
   for (int row = row0; row < row1; ++row) {
-    if (row > row0) look(row);
+    if (SHARE || row > row0) place(row);
+    if (b != unit_b || h != unit_h || tile != unit_tile) look();
     if (n == 1) continue;
     // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
     auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
@@ -387,7 +408,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1
     }
     if (lane == 0 && warp == 0) {
       p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-      if (p.lens[unit_b] < 0) atomicOr(p.err, kErrPage);
+      if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
     }
   }
 }
