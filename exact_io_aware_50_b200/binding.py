@@ -687,7 +687,8 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     place = q.device
     need = _fwd_cache_bytes(B, Hq, Hkv, Nq, d, page, max_pages)
     if workspace is None:
-        workspace = torch.empty(need, device=place, dtype=torch.uint8)
+        if need:
+            workspace = torch.empty(need, device=place, dtype=torch.uint8)
     elif (not workspace.is_cuda or not workspace.is_contiguous()
           or workspace.numel() * workspace.element_size() < need):
         raise ValueError(f"forward_cache: workspace must be a contiguous CUDA buffer of at least "
@@ -699,7 +700,7 @@ def forward_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, scal
     lse = torch.empty(B, Hq, Nq, device=place, dtype=_F32)
     _call(L.fa_fwd_cache, "fa_fwd_cache", dev, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-          lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
+          lens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr() if need else None, B, Hq, Hkv, Nq, d,
           page, num_pages, max_pages, d ** -0.5 if scale is None else scale,
           1 if causal else 0)
     return o, lse

@@ -47,6 +47,13 @@ constexpr float kShift = 12.f;                  // weights are stored times 2^12
 template <int D>
 struct RowCfg {
   static constexpr int ROWS = 16;
+  // CTAs take whole units where the block table has room for this many tokens.
+  // Measured, us a call in a graph with the line and with whole units, Hkv 8, Hq 32:
+  // d = 64, 512 tokens, B 1 7.9 / 6.5, B 64 20.6 / 14.0; d = 128, 256 tokens 8.2 / 6.3
+  // and 16.6 / 13.2, 512 tokens 8.0 / 8.4 and 24.0 / 19.0 (and a launch less, 3 us of
+  // the host's time); d = 256, 256 tokens 9.0 / 9.0 and 25.4 / 20.7, 512 tokens 8.8 /
+  // 12.9 and 41.8 / 33.0.
+  static constexpr int WHOLE = D == 256 ? 256 : 512;
   // A unit's start counts as four granules.  Measured, us a call in a graph
   // with 0 / 2 / 4 / 6: one sequence of 16384 tokens (Hq 32, Hkv 8, d 128) 16.3 /
   // 15.2 / 14.1 / 14.1; 32 ragged ones to 16384 104.7 / 103.0 / 100.4 / 100.5;
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
   const int g = lane >> 2, t = lane & 3;
   launch_dependents();   // the merge kernel's CTAs may take their places
   Run<typename C::L> run;
-  if (!run.start(p) || !run.next(p)) return;
+  if (!run.start(p) || !run.next<D>(p, warp == 0)) return;
 
   const uint32_t sbase = smem_u32(smem), ring = sbase + warp * kRing;
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE) + warp * kStages * C::NS;
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       if (t == 0) stat[warp * C::ROWS + g + 8 * e] = v == 0.f ? -INFINITY : m_s[e] + log2f(v);
     }
     __syncthreads();   // every warp is done with q and its ring
-    const bool more = run.next(p);
+    const bool more = run.next<D>(p, warp == 0);
     if (more) begin(st);
 
     // ---- the four warps' results joined
@@ -600,9 +607,9 @@ bool few_rows(const CacheArgs &a) {
 
 FwdCachePlan plan_of(const CacheArgs &a) {
   if (!few_rows(a)) return fwd_cache_tile_plan(a);
-  return a.d == 64    ? fwd_cache_plan<RowCfg<64>::L>(a, kMaxCtas)
-         : a.d == 128 ? fwd_cache_plan<RowCfg<128>::L>(a, kMaxCtas)
-                      : fwd_cache_plan<RowCfg<256>::L>(a, kMaxCtas);
+  return a.d == 64    ? fwd_cache_plan<RowCfg<64>::L>(a, kMaxCtas, RowCfg<64>::WHOLE)
+         : a.d == 128 ? fwd_cache_plan<RowCfg<128>::L>(a, kMaxCtas, RowCfg<128>::WHOLE)
+                      : fwd_cache_plan<RowCfg<256>::L>(a, kMaxCtas, RowCfg<256>::WHOLE);
 }
 
 }  // namespace

@@ -30,6 +30,7 @@ struct FwdCacheParams {
   int B, Hq, Hkv, Nq, g, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
   int page_log2, num_pages, max_pages;
   int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
+  int whole;                 // CTAs take whole units in turn: no line, no partials, no merge
   float scale_log2;
   unsigned long long g_inv;   // ceil(2^64 / g), 0 for g = 1
   unsigned *err;
@@ -79,7 +80,9 @@ __device__ __forceinline__ int warp_sum(int v) {
 // launcher checks), which is cut into p.ctas even runs.  A unit that begins in a
 // run costs its CTA some time before and after its granules: each unit stands in
 // the line with START empty granules in front, so that a CTA that ends one unit
-// and begins another gets less of them.
+// and begins another gets less of them.  Where the block table has room for few
+// tokens only (p.whole), CTA c takes units c, c + p.ctas, ... from end to end
+// instead, and there is nothing to merge.
 //
 // QMAJOR: row r of a head is query r / g of its group's head r % g, so a tile
 // holds consecutive queries and, causal, sees no further than its last one;
@@ -175,10 +178,10 @@ struct Line {
   }
 };
 
-// A CTA's run of the line, piece by piece.
+// A CTA's run of the line, piece by piece, or its units (p.whole).
 template <class L>
 struct Run {
-  int pos, end;        // granules left: [pos, end)
+  int pos, end;        // granules left: [pos, end); units pos, pos + p.ctas, ... below end
   int b, b_first;      // the sequence of the current piece, the line's granules before it
   // the current piece: granules [g0, g1) of ng of the unit (b, h, tile from
   // row r0 on), tokens [.., stop) of the sequence's len
@@ -186,6 +189,11 @@ struct Run {
 
   __device__ __forceinline__ bool start(const FwdCacheParams &p) {
     const int lane = threadIdx.x & 31;
+    if (p.whole) {
+      pos = blockIdx.x;
+      end = p.B * p.Hkv * p.tiles;
+      return pos < end;
+    }
     if (p.B <= 32) {   // one look at the lengths
       const int n = lane < p.B ? L::head(p, L::len(p, lane)) : 0;
       int inc = n;
@@ -214,8 +222,37 @@ struct Run {
     end = min(total, pos + per);
     return pos < end;
   }
-  __device__ __forceinline__ bool next(const FwdCacheParams &p) {
-    while (pos < end) {
+  // O = 0, L = -inf for the rows of the unit.
+  template <int D>
+  __device__ __forceinline__ void nothing(const FwdCacheParams &p) const {
+    const int lane = threadIdx.x & 31, rows = min(L::ROWS, p.R - r0);
+    const long long head = ((long long)b * p.Hkv + h) * p.R;
+    for (int i = lane; i < rows * (D / 8); i += 32) {
+      const int r = r0 + i / (D / 8), c = i % (D / 8);
+      const long long row = head + (L::QMAJOR ? r % p.g * p.Nq + r / p.g : r);
+      reinterpret_cast<uint4 *>(p.o + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (c == 0) p.lse[row] = -INFINITY;
+    }
+    if (lane == 0 && p.lens[b] < 0) atomicOr(p.err, kErrPage);
+  }
+  // On to the next piece; whole units that see no token are written here, by the
+  // warp that `writes`.
+  template <int D>
+  __device__ __forceinline__ bool next(const FwdCacheParams &p, bool writes) {
+    while (p.whole && pos < end) {
+      const int bh = pos / p.tiles, tile = pos - bh * p.tiles;
+      pos += p.ctas;
+      b = bh / p.Hkv;
+      h = bh - b * p.Hkv;
+      r0 = tile * L::ROWS;
+      len = L::len(p, b);
+      g0 = 0;
+      g1 = ng = L::granules(p, len, tile);
+      stop = min(len, ng * L::GRANULE);
+      if (ng > 0) return true;
+      if (writes) nothing<D>(p);
+    }
+    while (!p.whole && pos < end) {
       len = L::len(p, b);
       int n = L::head(p, len);
       while (pos - b_first >= n * p.Hkv) {   // on to the next sequence with tokens
@@ -417,6 +454,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1
 // then wait for the main kernel's end.
 template <int D, class L>
 int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
+  if (p.whole) return 0;
   const long long rows = (long long)p.B * p.Hq * p.Nq, units = (long long)p.B * p.Hkv * p.tiles;
   // A warp a row: about eight pieces a unit, or fewer, or more rows than CTAs that
   // run at once.  Measured, a call: Hq 16, Hkv 4, d 256, B 8, 2304 tokens, 4 queries
@@ -442,21 +480,25 @@ int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
 }
 
 // What the host knows of the work of a line: CTAs (fewer than `most_ctas` when
-// the block table has room for fewer granules), rows of a partial.
+// the block table has room for fewer granules), rows of a partial; whether the table
+// has room for so few tokens (`whole_tokens`) that CTAs take whole units.
 struct FwdCachePlan {
   double R, most;   // most: the line's length when every sequence fills its table
   long long tiles;
   int prows, ctas;
+  bool whole;
 };
 template <class L>
-FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas) {
+FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas, int whole_tokens) {
   FwdCachePlan x;
   x.R = (double)(a.Hq / a.Hkv) * a.Nq;
   x.prows = x.R < L::ROWS ? (int)x.R : L::ROWS;
   x.tiles = (long long)((x.R + L::ROWS - 1) / L::ROWS);
   x.most = (double)a.B * a.Hkv * x.tiles *
            (((long long)a.max_pages * a.page + L::GRANULE - 1) / L::GRANULE + L::START);
-  x.ctas = x.most < most_ctas ? (int)x.most : most_ctas;
+  x.whole = (long long)a.max_pages * a.page <= whole_tokens;
+  const double parts = x.whole ? (double)a.B * a.Hkv * x.tiles : x.most;
+  x.ctas = parts < most_ctas ? (int)parts : most_ctas;
   return x;
 }
 // The kernel for many query rows (fa_fwd_cache_sm100.cu).
@@ -464,7 +506,7 @@ FwdCachePlan fwd_cache_tile_plan(const CacheArgs &a);
 int launch_fwd_cache_tiles(const CacheArgs &a, const FwdCachePlan &x);
 
 inline size_t fwd_cache_plan_bytes(const FwdCachePlan &x, int d) {
-  return (size_t)x.ctas * 2 * x.prows * (d + 1) * 4;
+  return x.whole ? 0 : (size_t)x.ctas * 2 * x.prows * (d + 1) * 4;
 }
 inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x) {
   FwdCacheParams p;
@@ -481,7 +523,7 @@ inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x
   p.tiles = (int)x.tiles;
   p.page_log2 = a.page == 16 ? 4 : a.page == 32 ? 5 : a.page == 64 ? 6 : 7;
   p.num_pages = a.num_pages; p.max_pages = a.max_pages;
-  p.causal = a.causal; p.ctas = x.ctas; p.prows = x.prows;
+  p.causal = a.causal; p.ctas = x.ctas; p.prows = x.prows; p.whole = x.whole;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.err = a.err;
   return p;

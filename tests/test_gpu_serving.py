@@ -351,6 +351,18 @@ def test_attention(c):
     check_attention(q, cache, table, lens, page, causal)
 
 
+@pytest.mark.parametrize("c", ATTN, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+def test_attention_wide_table(c):
+    """The same lengths in a block table with room for many more tokens, whose
+    other entries are no pages."""
+    B, Hq, Hkv, Nq, d, page, lens, causal = c
+    cache, table = attention_case(B, Hkv, d, page, lens, seed=Nq + d)
+    table = torch.cat([table, torch.full((B, 700 // page), -1, dtype=torch.int32)], dim=1)
+    assert F.fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, table.shape[1]) > 0
+    q = torch.randn(B, Hq, Nq, d, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    check_attention(q, cache, table, lens, page, causal)
+
+
 @pytest.mark.parametrize("c", [   # many tiles of 128 or 256 rows a head
     (2, 3, 1, 700, 64, 16, [700, 90], True),         # an odd group; most queries of the second see nothing
     (1, 5, 1, 301, 128, 32, [1000], True),
@@ -362,6 +374,17 @@ def test_attention(c):
 ], ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
 def test_many_tiles(c):
     test_attention(c)
+
+
+def test_whole_units_many_and_empty():
+    """Tables of few tokens, where CTAs take units from end to end: more units than
+    CTAs, and sequences and queries that see nothing."""
+    for c in [(40, 16, 8, 1, 64, 16, [(37 * b) % 300 if b % 3 else 0 for b in range(40)], True),
+              (150, 3, 3, 1, 128, 32, [(11 * b) % 97 for b in range(150)], False),
+              (9, 6, 2, 70, 128, 16, [0, 1, 69, 70, 71, 200, 5, 0, 31], True),
+              (5, 2, 2, 130, 256, 64, [0, 64, 129, 1, 130], True)]:
+        assert F.fa_fwd_cache_workspace_size(c[0], c[1], c[2], c[3], c[4], c[5], max(c[6]) // c[5] + 2) == 0
+        test_attention(c)
 
 
 @pytest.mark.parametrize("spread", [0.0, 4.0])
