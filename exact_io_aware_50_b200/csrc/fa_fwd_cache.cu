@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
   const int g = lane >> 2, t = lane & 3;
   launch_dependents();   // the merge kernel's CTAs may take their places
   Run<typename C::L> run;
-  if (!run.start(p) || !run.next<D>(p, warp == 0)) return;
+  if (!run.start(p) || !run.template next<D>(p, warp == 0)) return;
 
   const uint32_t sbase = smem_u32(smem), ring = sbase + warp * kRing;
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE) + warp * kStages * C::NS;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       if (t == 0) stat[warp * C::ROWS + g + 8 * e] = v == 0.f ? -INFINITY : m_s[e] + log2f(v);
     }
     __syncthreads();   // every warp is done with q and its ring
-    const bool more = run.next<D>(p, warp == 0);
+    const bool more = run.template next<D>(p, warp == 0);
     if (more) begin(st);
 
     // ---- the four warps' results joined

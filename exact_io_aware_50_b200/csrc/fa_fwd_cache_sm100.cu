@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
     Run<typename C::L> run;
     bool more = run.start(p);
     for (; ok; ++u) {
-      if (more) more = run.next<D>(p, warp == C::SOFT);
+      if (more) more = run.template next<D>(p, warp == C::SOFT);
       const int n = more ? run.g1 - run.g0 : 0;
       if (leader) {
         ok = bounded_wait(bar(B_UEMPTY + (u & 1)), ((u >> 1) & 1) ^ 1, wc);

@@ -310,6 +310,91 @@ constexpr int kMergeCtas = 148 * 16;   // of warps a row, at most
 template <class L, int W>
 constexpr int merge_ahead() { return W == 1 && L::QMAJOR ? 4 : 8; }
 
+// Row `row` of O and L from its unit's n pieces (n = 0: nothing), row rr of the
+// tile, the first of CTA c0; warp w of W.
+template <int D, class L, int W>
+__device__ __forceinline__ void merge_row(const FwdCacheParams &p, int row, int rr, int c0, int n, int warp, int lane,
+                                          float (*s_o)[D], float *s_w) {
+  // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
+  auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
+  constexpr int PER = D / 32, AHEAD = merge_ahead<L, W>();
+  const float *src = p.o_part + lane * PER;
+  // warp w adds pieces w, w + W, ...: the first loads go out before the weights are known
+  float v[AHEAD][PER];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
+  // lane i looks at pieces i, i + 32, ...
+  const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
+  float top = mine;
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
+  float sum = own;
+  if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
+  for (int i = lane + 32; i < n; i += 32) {
+    const float x = p.l_part[at(i)];
+    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+    sum += w;
+    if (W > 1 && i % W == warp) s_w[i] = w;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  __syncwarp();
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += AHEAD * W) {
+    if (i0 != warp) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (i0 + W * k < n) load_floats<PER>(src + at(i0 + W * k) * D, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (i0 + W * k < n) {
+        const int i = i0 + W * k;
+        float w;
+        if (W > 1) {
+          w = s_w[i];
+        } else {
+          w = __shfl_sync(0xffffffffu, own, i & 31);
+          if (i >= 32) {   // more pieces than lanes: the weight again
+            const float x = p.l_part[at(i)];
+            w = x == -INFINITY ? 0.f : fast_exp2(x - top);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+      }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] *= inv;
+  __nv_bfloat16 *dst = p.o + (long long)row * D;
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        x += s_o[w][2 * threadIdx.x];
+        y += s_o[w][2 * threadIdx.x + 1];
+      }
+      reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+      reinterpret_cast<uint32_t *>(dst)[(lane * PER + e) / 2] = pack_bf16x2(acc[e], acc[e + 1]);
+  }
+  if (lane == 0 && warp == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
 template <int D, class L, int W>
 __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1 : D == 256 ? 3 : 4) fwd_cache_merge_kernel(const FwdCacheParams p, int each) {
   __shared__ float s_o[W > 1 ? kMergeWarps : 1][D], s_w[kMaxCtas];
@@ -366,85 +451,57 @@ __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1
     if (SHARE || row > row0) place(row);
     if (b != unit_b || h != unit_h || tile != unit_tile) look();
     if (n == 1) continue;
-    // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
-    auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
-    constexpr int PER = D / 32, AHEAD = merge_ahead<L, W>();
-    const float *src = p.o_part + lane * PER;
-    // warp w adds pieces w, w + W, ...: the first loads go out before the weights are known
-    float v[AHEAD][PER];
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
-    // lane i looks at pieces i, i + 32, ...
-    const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
-    float top = mine;
-    for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
-    float sum = own;
-    if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
-    for (int i = lane + 32; i < n; i += 32) {
-      const float x = p.l_part[at(i)];
-      const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-      sum += w;
-      if (W > 1 && i % W == warp) s_w[i] = w;
+    merge_row<D, L, W>(p, row, rr, c0, n, warp, lane, s_o, s_w);
+    if (lane == 0 && warp == 0 && p.lens[b] < 0) atomicOr(p.err, kErrPage);
+  }
+}
+
+// The same where units are more than twice the CTAs, most of them whole: CTA (x, c) takes eight rows
+// of the one unit that begins in run c and does not end there.  Units that see no
+// token are looked for only if a sequence has one.  Measured, a call by rows / by
+// CTAs, causal, Hq 32, Hkv 8, d 128: B 1, 2048 queries (256 units) 110 / 117 us; B 8, 512
+// of 1024 tokens (512 units) 178 / 164; B 32, 512 of 512 (2048 units) 398 / 305.
+template <int D, class L>
+__global__ void __launch_bounds__(kMergeWarps * 32, D == 256 ? 3 : 4) fwd_cache_merge_split_kernel(const FwdCacheParams p) {
+  __shared__ int s_unit[5];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y;
+  if (warp == 0) {
+    bool empty = false;   // a tile of some sequence sees no token
+    for (int i = lane; i < p.B; i += 32) empty |= L::granules(p, L::len(p, i), 0) == 0;
+    empty = __any_sync(0xffffffffu, empty);
+    int total, unused, b = 0, h = 0, tile = 0, n = 0;
+    L::sums(p, 0, &total, &unused);
+    total *= p.Hkv;
+    const int per = max((total + p.ctas - 1) / p.ctas, 1), end = min(total, per * (c + 1));
+    if (per * c < end) {
+      const int pos = end - 1;   // the unit that the run ends in
+      int before;
+      b = L::sequence_at(p, pos / p.Hkv, &before);
+      const int len = L::len(p, b), head = L::head(p, len);
+      h = (pos - before * p.Hkv) / head;
+      int at = pos - before * p.Hkv - h * head;
+      tile = L::tile_at(p, len, at);
+      const int first = pos - at + L::START, last = pos - at + L::span(p, len, tile) - 1;   // its granules
+      n = first / per == c ? last / per - c + 1 : 1;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    __syncwarp();
-    float acc[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-#pragma unroll 1
-    for (int i0 = warp; i0 < n; i0 += AHEAD * W) {
-      if (i0 != warp) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-          if (i0 + W * k < n) load_floats<PER>(src + at(i0 + W * k) * D, v[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (i0 + W * k < n) {
-          const int i = i0 + W * k;
-          float w;
-          if (W > 1) {
-            w = s_w[i];
-          } else {
-            w = __shfl_sync(0xffffffffu, own, i & 31);
-            if (i >= 32) {   // more pieces than lanes: the weight again
-              const float x = p.l_part[at(i)];
-              w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-        }
+    if (lane == 0) {
+      s_unit[0] = b * p.Hkv + h; s_unit[1] = tile; s_unit[2] = n; s_unit[3] = empty;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] *= inv;
-    __nv_bfloat16 *dst = p.o + (long long)row * D;
-    if constexpr (W > 1) {
-#pragma unroll
-      for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = acc[e];
-      __syncthreads();
-      if (threadIdx.x < D / 2) {
-        float x = 0.f, y = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          x += s_o[w][2 * threadIdx.x];
-          y += s_o[w][2 * threadIdx.x + 1];
-        }
-        reinterpret_cast<uint32_t *>(dst)[threadIdx.x] = pack_bf16x2(x, y);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < PER; e += 2)
-        reinterpret_cast<uint32_t *>(dst)[(lane * PER + e) / 2] = pack_bf16x2(acc[e], acc[e + 1]);
-    }
-    if (lane == 0 && warp == 0) {
-      p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  }
+  // every CTA waits, so that what follows in the stream finds o and lse whole
+  wait_for_primary();
+  __syncthreads();
+  const int bh = s_unit[0], rr = blockIdx.x * kMergeWarps + warp, r = s_unit[1] * L::ROWS + rr, n = s_unit[2];
+  if (n > 1 && rr < L::ROWS && r < p.R)
+    merge_row<D, L, 1>(p, bh * p.R + r % p.g * p.Nq + r / p.g, rr, c, n, 0, lane, nullptr, nullptr);
+  if (!s_unit[3]) return;
+  const long long warps = (long long)gridDim.x * gridDim.y * kMergeWarps, rows = (long long)p.B * p.Hq * p.Nq;
+  for (long long row = ((long long)c * gridDim.x + blockIdx.x) * kMergeWarps + warp; row < rows; row += warps) {
+    const int b = (int)(row / (p.Hq * p.Nq)), q = (int)(row % (p.Hq * p.Nq)), i = q % p.Nq, head = q / p.Nq % p.g;
+    if (L::granules(p, L::len(p, b), (int)(((long long)i * p.g + head) / L::ROWS))) continue;
+    for (int x = lane; x < D / 8; x += 32) reinterpret_cast<uint4 *>(p.o + row * D)[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) {
+      p.lse[row] = -INFINITY;
       if (p.lens[b] < 0) atomicOr(p.err, kErrPage);
     }
   }
@@ -473,6 +530,13 @@ int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if constexpr (L::QMAJOR) {
+    if (units > 2 * p.ctas) {
+      cfg.gridDim = dim3((unsigned)((p.prows + kMergeWarps - 1) / kMergeWarps), (unsigned)p.ctas, 1);
+      return cudaLaunchKernelEx(&cfg, fwd_cache_merge_split_kernel<D, L>, p) == cudaSuccess &&
+             cudaGetLastError() == cudaSuccess ? 0 : 5;
+    }
+  }
   if ((many ? cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, 1>, p, (int)each)
             : cudaLaunchKernelEx(&cfg, fwd_cache_merge_kernel<D, L, kMergeWarps>, p, 1)) != cudaSuccess)
     return 5;

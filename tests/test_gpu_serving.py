@@ -371,6 +371,9 @@ def test_attention_wide_table(c):
     (1, 6, 6, 517, 64, 64, [517], True),
     (1, 4, 1, 1100, 128, 16, [1100], False),
     (2, 64, 1, 400, 64, 32, [600, 433], True),       # 100 tiles; a warp of the merge takes several rows
+    (8, 64, 2, 200, 64, 16, [900, 0, 130, 201, 1, 77, 640, 0], True),   # far more units than CTAs, some of them empty
+    (3, 32, 8, 400, 256, 64, [600, 0, 250], True),
+    (8, 64, 2, 200, 128, 16, [900, 0, 1, 201, 0, 64, 500, 30], False),
 ], ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
 def test_many_tiles(c):
     test_attention(c)
