@@ -8,6 +8,11 @@
 // leave E4M3's normal range.  Memory-bound: es bytes read and one written an
 // element (es + 1 reading back); both kernels move 16 bytes of the wider side at
 // a time.
+//
+// Measured on B200, bf16, Hkv 8, d 128, pages of 64: 4 x 4096 tokens written (82 MB)
+// 18.1 us = 4.5 TB/s, 69 % of a plain copy's rate: a CTA's stores wait for the maximum
+// over its page, so loads and stores overlap between CTAs only; 64 x 1 token 2.9 us,
+// a launch; 4 x 5001 to 8192 tokens read back (192 MB) 33.5 us = 5.7 TB/s, 87 %.
 #include "cache.cuh"
 
 namespace fa {

@@ -29,6 +29,16 @@
 // It has a reference M of its own, the running maximum of s + log2 sv: terms
 // down to 2^-26 of the largest keep 11 bits whatever the pages' scales, and
 // smaller ones err by at most 2^-37 of the largest weight.
+//
+// Measured on B200, a call in a graph, Hq 32, Hkv 8, d 128: 32 sequences of 2047 to
+// 16384 tokens (612 MB) 101 us = 6.0 TB/s, 92 % of a plain copy's rate, the bound of
+// long batches; one of 16384 tokens 14.4 us, of which 7 are the latency of a call's
+// two launches, the page look-up, the first copies and the merge.  d = 256 holds O in
+// 128 registers a thread: B 8, Hq 16, Hkv 4, 16384 tokens 50 us = 5.3 TB/s.  Many
+// short sequences are bound by a unit's start and end, about 4 us of a CTA: 256 of
+// 256 tokens 45 us = 3.0 TB/s.  Looking up the next unit's pages and copying its first
+// steps before this one's last did not shorten that (2 to 5 % slower), nor did copies
+// by TMA (boxes of 2 to 8 KB, one CTA an SM: 130 us where this form took 109).
 #include <type_traits>
 
 #include "fwd_cache.cuh"

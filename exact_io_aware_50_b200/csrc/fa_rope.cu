@@ -13,6 +13,10 @@
 // the fraction of the turn at t, whose upper 32 bits go to float32.  So the
 // reduction costs an integer product, and a position of millions keeps its
 // angle: 2^-32 of a turn beside what float64 rounds in f_p / 2 pi, times t.
+//
+// Measured on B200: bf16, B 4, 16 + 16 heads, N 4096, d 128 (268 MB) 44.9 us = 6.0
+// TB/s, 91 % of a plain copy's rate; float32, B 2, 16 + 4 heads, N 1999, d 64 (41 MB)
+// 8.4 us; one token of 32 sequences 2.5 us, which is what a launch takes.
 #include "common.cuh"
 #include "launch.h"
 

@@ -281,9 +281,9 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o,
  *     (x, y) -> mscale * (x cos a - y sin a, y cos a + x sin a).
  * interleaved == 0: x is column p, y column p + rot_dim / 2 (halves);
  * interleaved != 0: x is column 2p, y column 2p + 1.  Columns rot_dim and up
- * are copied.  The angle is formed and reduced in float64 (positions of
- * millions keep their angle), the rotation runs in float32 and is rounded
- * once to the tensors' type.
+ * are copied.  The angle is reduced as a 64-bit fraction of a turn, formed from
+ * the float64 frequency (positions of millions keep their angle); the rotation
+ * runs in float32 and is rounded once to the tensors' type.
  *
  * q, q_out [B, Hq, N, d]; k, k_out [B, Hkv, N, d]: bfloat16 (fa_rope,
  * fa_rope_bwd) or float32 (the _f32 forms); one launch turns both.  k and
@@ -411,7 +411,7 @@ int fa_cache_read_f32(const void *k_cache, const void *v_cache, const float *k_s
  * k_scale, v_scale: finite and > 0, as fa_cache_append writes them.
  *
  * workspace: fa_fwd_cache_workspace_size(...) bytes, 256-byte aligned
- * (NULL when that is 0); contents ignored on entry and clobbered, so calls
+ * (NULL when that is 0, as for tables of few tokens); contents ignored on entry and clobbered, so calls
  * that may overlap on the GPU (two graphs, two streams) need one each.
  */
 size_t fa_fwd_cache_workspace_size(int B, int Hq, int Hkv, int Nq, int d, int page, int max_pages);
