@@ -191,11 +191,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
   // ---- copies.  Lane i holds the page number of the warp's subtile 32 k + i
   // of the piece, and of the 32 after them.
   int cur, nxt;
+  constexpr int kNoToken = -2147483647 - 1;
   auto token_of = [&](int i) { return (run.g0 + i) * kGranule + warp * kSub; };
-  auto lookup = [&](int i) {
+  // fetched first and looked at later, so that a load is not waited for
+  auto fetch = [&](int i) {
     const int j = token_of(i);
-    if (j >= run.stop) return -1;
-    return checked_page(p.table + (long long)run.b * p.max_pages, j >> p.page_log2, p.num_pages, p.err);
+    return j >= run.stop ? kNoToken : p.table[(long long)run.b * p.max_pages + (j >> p.page_log2)];
+  };
+  auto checked = [&](int pg) {
+    if ((unsigned)pg < (unsigned)p.num_pages) return pg;
+    if (pg != kNoToken) atomicOr(p.err, kErrPage);
+    return -1;
+  };
+  auto fetch_first = [&]() {
+    cur = fetch(lane);
+    nxt = run.g1 - run.g0 > 32 ? fetch(32 + lane) : kNoToken;
   };
   // Step s of the piece into stage st; always one commit group a step.  What
   // is no token of the piece becomes zeros, and its page's scales too.
@@ -203,8 +213,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     const int i0 = s * C::NS;
     if (i0 < run.g1 - run.g0) {
       if (i0 && (i0 & 31) == 0) {
-        cur = nxt;
-        nxt = lookup(i0 + 32 + lane);
+        cur = checked(nxt);
+        nxt = fetch(i0 + 32 + lane);
       }
 #pragma unroll
       for (int n = 0; n < C::NS; ++n) {
@@ -234,26 +244,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     }
     cp_async_commit();
   };
-  // The piece's pages, q rows and first AHEAD steps, from stage st on.
+  // The piece's q rows and, its first pages fetched, first AHEAD steps, from stage st on.
   auto begin = [&](int st) {
-    cur = lookup(lane);
-    nxt = run.g1 - run.g0 > 32 ? lookup(32 + lane) : -1;
     const int rows = min(C::ROWS, p.R - run.r0);
     const uint8_t *q = (const uint8_t *)(p.q + (((long long)run.b * p.Hkv + run.h) * p.R + run.r0) * D);
     for (int i = threadIdx.x; i < rows * 2 * C::CH; i += kWarps * 32)   // a head's R rows lie together
       cp_async16<0>(sbase + C::OFF_Q + i / (2 * C::CH) * C::QROW + i % (2 * C::CH) * 16, q + i * 16);
+    cur = checked(cur);
 #pragma unroll
     for (int k = 0; k < C::AHEAD; ++k) issue(k, (st + k) % kStages);
     if (threadIdx.x == 0) (void)checked_len(p.lens, run.b, p.max_pages, 1 << p.page_log2, p.err);
   };
 
   int st = 0;   // stage of the step at hand
+  fetch_first();
   begin(st);
   while (true) {
     // the piece at hand (`run` moves on before its merge)
     const int subs = run.g1 - run.g0, steps = (subs + C::NS - 1) / C::NS;
     const int rows = min(C::ROWS, p.R - run.r0), len = run.len, stop = run.stop;
     const int token = token_of(0);   // of this warp; its subtile i starts kGranule * i later
+    const bool two = rows > 8;       // else a lane's second row does not exist: no work for it
 
     // ---- q: A fragments of halves, each row times a power of two
     cp_async_wait<C::AHEAD - 1>();   // q came with the first step
@@ -266,6 +277,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
       const bool live = r < rows;
+      row_c[e] = 0.f;
+      lim[e] = 0;
+      if (e && !two) {
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) qa[c][1] = qa[c][3] = 0u;
+        continue;
+      }
       const uint8_t *src = smem + C::OFF_Q + r * C::QROW + 8 * t;
       uint2 raw[C::CH];
       float mx = 0.f;
@@ -373,6 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int n = 0; n < C::NS; ++n) {
+          if (e && !two) continue;
           const float cf = row_c[e] * sk[n];
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[2 * n + (i >> 1)][2 * e + (i & 1)] *= cf;
@@ -382,6 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int n = 0; n < C::NS; ++n) {
+            if (e && !two) continue;
             const int seen = min(nv[n], lim[e] - j0[n]) - 2 * t;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -393,6 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mxs[e] = mxo[e] = -INFINITY;
+        if (e && !two) continue;
 #pragma unroll
         for (int n = 0; n < C::NS; ++n) {
           float mx = -INFINITY;
@@ -406,6 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          if (e && !two) continue;
           float vs = mxs[e], vo = mxo[e];
           vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
           vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 1));
@@ -428,6 +450,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       uint32_t pa[C::NS][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if (e && !two) {
+#pragma unroll
+          for (int n = 0; n < C::NS; ++n) pa[n][1] = pa[n][3] = 0u;
+          continue;
+        }
         const bool none = m_s[e] == -INFINITY;
         const float ms = none ? 0.f : m_s[e];
         const float diff = none ? 0.f : m_s[e] - m_o[e] + kShift;
@@ -511,12 +538,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       st = st + 1 == kStages ? 0 : st + 1;
     }
 
-    // ---- on to the next piece: its first copies go out before the merge
+    // ---- on to the next piece: its pages are looked up, and its first copies go
+    // out before the merge
     const long long row0 = ((long long)run.b * p.Hkv + run.h) * p.R + run.r0;
     const int part = run.part(p);
+    const bool more = run.template next<D>(p, warp == 0);
+    if (more) fetch_first();
     // each row's log-sum-exp in this warp
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      if (e && !two) continue;
       float v = l[e];
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -524,7 +555,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       if (t == 0) stat[warp * C::ROWS + g + 8 * e] = v == 0.f ? -INFINITY : m_s[e] + log2f(v);
     }
     __syncthreads();   // every warp is done with q and its ring
-    const bool more = run.template next<D>(p, warp == 0);
     if (more) begin(st);
 
     // ---- the four warps' results joined
@@ -536,6 +566,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
+      if (e && !two) continue;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
@@ -545,6 +576,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       f[e] = l[e] == 0.f ? 0.f
                          : fast_exp2(m_o[e] - kShift - m_s[e]) / l[e] *
                                (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
+      if (warp == 0 && t == 0 && r < rows) {
+        const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+        if (part < 0) p.lse[row0 + r] = L2 * 0.69314718055994531f;
+        else p.l_part[part + r] = L2;
+      }
     }
 #pragma unroll
     for (int half = 0; half < D / C::JOIN; ++half) {
@@ -577,16 +613,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
         else
           *reinterpret_cast<float4 *>(p.o_part + (long long)(part + r) * D + col) = a;
       }
-    }
-    if ((int)threadIdx.x < rows) {
-      const int r = threadIdx.x;
-      float top = -INFINITY, sum = 0.f;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
-      for (int w = 0; w < kWarps; ++w)
-        sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
-      const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-      if (part < 0) p.lse[row0 + r] = L2 * 0.69314718055994531f;
-      else p.l_part[part + r] = L2;
     }
     if (!more) return;
     // (the barrier before q is read frees the ring and the statistics)
