@@ -560,8 +560,10 @@ FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas, int whole_tokens)
   x.tiles = (long long)((x.R + L::ROWS - 1) / L::ROWS);
   x.most = (double)a.B * a.Hkv * x.tiles *
            (((long long)a.max_pages * a.page + L::GRANULE - 1) / L::GRANULE + L::START);
-  x.whole = (long long)a.max_pages * a.page <= whole_tokens;
-  const double parts = x.whole ? (double)a.B * a.Hkv * x.tiles : x.most;
+  const double units = (double)a.B * a.Hkv * x.tiles;
+  // twice the tokens where every CTA has a unit without a cut
+  x.whole = (long long)a.max_pages * a.page <= (units < most_ctas ? 1 : 2) * (long long)whole_tokens;
+  const double parts = x.whole ? units : x.most;
   x.ctas = parts < most_ctas ? (int)parts : most_ctas;
   return x;
 }
