@@ -62,8 +62,11 @@ struct RowCfg {
   // d = 64, 512 tokens, B 1 7.9 / 6.5, B 64 20.6 / 14.0; d = 128, 256 tokens 8.2 / 6.3
   // and 16.6 / 13.2, 512 tokens 8.0 / 8.4 and 24.0 / 19.0 (and a launch less, 3 us of
   // the host's time); d = 256, 256 tokens 9.0 / 9.0 and 25.4 / 20.7, 512 tokens 8.8 /
-  // 12.9 and 41.8 / 33.0.
-  static constexpr int WHOLE = D == 256 ? 256 : 512;
+  // 12.9 and 41.8 / 33.0.  With a unit for every CTA (B 64; B 50 ragged), d = 64, 2048
+  // tokens 31.4 / 29.9 and 25.7 / 25.7; d = 128, 1024 tokens 34.3 / 30.5 and 23.8 /
+  // 23.9, 2048 tokens 43.2 / 46.3 and 29.0 / 38.7; d = 256, 512 tokens 39.2 / 31.5 and
+  // 27.0 / 25.3, 1024 tokens 46.4 / 46.5 and 32.6 / 39.6.
+  static constexpr int WHOLE = D == 256 ? 256 : 512, WHOLE_MANY = D == 128 ? 1024 : D == 64 ? 2048 : 512;
   // A unit's start counts as four granules.  Measured, us a call in a graph
   // with 0 / 2 / 4 / 6: one sequence of 16384 tokens (Hq 32, Hkv 8, d 128) 16.3 /
   // 15.2 / 14.1 / 14.1; 32 ragged ones to 16384 104.7 / 103.0 / 100.4 / 100.5;
@@ -643,9 +646,9 @@ bool few_rows(const CacheArgs &a) {
 
 FwdCachePlan plan_of(const CacheArgs &a) {
   if (!few_rows(a)) return fwd_cache_tile_plan(a);
-  return a.d == 64    ? fwd_cache_plan<RowCfg<64>::L>(a, kMaxCtas, RowCfg<64>::WHOLE)
-         : a.d == 128 ? fwd_cache_plan<RowCfg<128>::L>(a, kMaxCtas, RowCfg<128>::WHOLE)
-                      : fwd_cache_plan<RowCfg<256>::L>(a, kMaxCtas, RowCfg<256>::WHOLE);
+  return a.d == 64    ? fwd_cache_plan<RowCfg<64>::L>(a, kMaxCtas, RowCfg<64>::WHOLE, RowCfg<64>::WHOLE_MANY)
+         : a.d == 128 ? fwd_cache_plan<RowCfg<128>::L>(a, kMaxCtas, RowCfg<128>::WHOLE, RowCfg<128>::WHOLE_MANY)
+                      : fwd_cache_plan<RowCfg<256>::L>(a, kMaxCtas, RowCfg<256>::WHOLE, RowCfg<256>::WHOLE_MANY);
 }
 
 }  // namespace

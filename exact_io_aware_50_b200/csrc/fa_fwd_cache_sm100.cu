@@ -45,8 +45,9 @@ constexpr int kThreads = 512;
 // Measured, us a call in a graph with the line and with whole units, causal, d 128, Hkv
 // 8: B 1, Hq 8, 128 queries of 128 tokens 14.7 / 10.3, 512 of 512 22.3 / 22.3, 64 of 512
 // 14.7 / 16.3; B 1, Hq 32, 512 of 512 37.4 / 21.9; B 8, Hq 32, 128 of 128 31.1 / 14.6,
-// 512 of 512 119.6 / 65.8.
-constexpr int kWholeTokens = 512;
+// 512 of 512 119.6 / 65.8.  With a unit for every CTA, B 8, 512 of 2048 238 / 198 (ragged
+// 207 / 177), 512 of 4096 387 / 368 (ragged 277 / 328).
+constexpr int kWhole = 512, kWholeMany = 2048;
 constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
 constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
@@ -655,7 +656,8 @@ bool two_tiles(const CacheArgs &a) { return a.d <= 128 && (double)(a.Hq / a.Hkv)
 }  // namespace
 
 FwdCachePlan fwd_cache_tile_plan(const CacheArgs &a) {
-  return two_tiles(a) ? fwd_cache_plan<TileCfg<128, 2>::L>(a, 148, kWholeTokens) : fwd_cache_plan<TileCfg<128, 1>::L>(a, 148, kWholeTokens);
+  return two_tiles(a) ? fwd_cache_plan<TileCfg<128, 2>::L>(a, 148, kWhole, kWholeMany)
+                      : fwd_cache_plan<TileCfg<128, 1>::L>(a, 148, kWhole, kWholeMany);
 }
 
 int launch_fwd_cache_tiles(const CacheArgs &a, const FwdCachePlan &x) {

@@ -545,7 +545,8 @@ int launch_fwd_cache_merge(const FwdCacheParams &p, cudaStream_t stream) {
 
 // What the host knows of the work of a line: CTAs (fewer than `most_ctas` when
 // the block table has room for fewer granules), rows of a partial; whether the table
-// has room for so few tokens (`whole_tokens`) that CTAs take whole units.
+// has room for so few tokens that CTAs take whole units: `whole`, or `whole_many` where
+// every CTA has a unit without a cut.
 struct FwdCachePlan {
   double R, most;   // most: the line's length when every sequence fills its table
   long long tiles;
@@ -553,7 +554,7 @@ struct FwdCachePlan {
   bool whole;
 };
 template <class L>
-FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas, int whole_tokens) {
+FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas, int whole, int whole_many) {
   FwdCachePlan x;
   x.R = (double)(a.Hq / a.Hkv) * a.Nq;
   x.prows = x.R < L::ROWS ? (int)x.R : L::ROWS;
@@ -561,8 +562,7 @@ FwdCachePlan fwd_cache_plan(const CacheArgs &a, int most_ctas, int whole_tokens)
   x.most = (double)a.B * a.Hkv * x.tiles *
            (((long long)a.max_pages * a.page + L::GRANULE - 1) / L::GRANULE + L::START);
   const double units = (double)a.B * a.Hkv * x.tiles;
-  // twice the tokens where every CTA has a unit without a cut
-  x.whole = (long long)a.max_pages * a.page <= (units < most_ctas ? 1 : 2) * (long long)whole_tokens;
+  x.whole = (long long)a.max_pages * a.page <= (units < most_ctas ? whole : whole_many);
   const double parts = x.whole ? units : x.most;
   x.ctas = parts < most_ctas ? (int)parts : most_ctas;
   return x;

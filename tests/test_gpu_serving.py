@@ -351,19 +351,23 @@ def test_attention(c):
     check_attention(q, cache, table, lens, page, causal)
 
 
-@pytest.mark.parametrize("c", ATTN, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
-def test_attention_wide_table(c):
+def check_wide_table(c, more):
     """The same lengths in a block table with room for many more tokens, whose
     other entries are no pages."""
     B, Hq, Hkv, Nq, d, page, lens, causal = c
     cache, table = attention_case(B, Hkv, d, page, lens, seed=Nq + d)
-    table = torch.cat([table, torch.full((B, 700 // page), -1, dtype=torch.int32)], dim=1)
+    table = torch.cat([table, torch.full((B, more // page), -1, dtype=torch.int32)], dim=1)
     assert F.fa_fwd_cache_workspace_size(B, Hq, Hkv, Nq, d, page, table.shape[1]) > 0
     q = torch.randn(B, Hq, Nq, d, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
     check_attention(q, cache, table, lens, page, causal)
 
 
-@pytest.mark.parametrize("c", [   # many tiles of 128 or 256 rows a head
+@pytest.mark.parametrize("c", ATTN, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+def test_attention_wide_table(c):
+    check_wide_table(c, 700)
+
+
+MANY = [  # many tiles of 128 or 256 rows a head
     (2, 3, 1, 700, 64, 16, [700, 90], True),         # an odd group; most queries of the second see nothing
     (1, 5, 1, 301, 128, 32, [1000], True),
     (3, 8, 1, 220, 128, 64, [0, 221, 5], True),
@@ -374,9 +378,17 @@ def test_attention_wide_table(c):
     (8, 64, 2, 200, 64, 16, [900, 0, 130, 201, 1, 77, 640, 0], True),   # far more units than CTAs, some of them empty
     (3, 32, 8, 400, 256, 64, [600, 0, 250], True),
     (8, 64, 2, 200, 128, 16, [900, 0, 1, 201, 0, 64, 500, 30], False),
-], ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
 def test_many_tiles(c):
     test_attention(c)
+
+
+@pytest.mark.parametrize("c", MANY, ids=lambda c: "x".join(map(str, c)).replace(" ", ""))
+def test_many_tiles_wide_table(c):
+    check_wide_table(c, 2100)
 
 
 def test_whole_units_many_and_empty():
