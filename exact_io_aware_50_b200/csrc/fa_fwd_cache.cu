@@ -194,21 +194,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
   // ---- copies.  Lane i holds the page number of the warp's subtile 32 k + i
   // of the piece, and of the 32 after them.
   int cur, nxt;
-  constexpr int kNoToken = -2147483647 - 1;
   auto token_of = [&](int i) { return (run.g0 + i) * kGranule + warp * kSub; };
   // fetched first and looked at later, so that a load is not waited for
   auto fetch = [&](int i) {
     const int j = token_of(i);
-    return j >= run.stop ? kNoToken : p.table[(long long)run.b * p.max_pages + (j >> p.page_log2)];
+    return j >= run.stop ? 0 : p.table[(long long)run.b * p.max_pages + (j >> p.page_log2)];
   };
-  auto checked = [&](int pg) {
+  auto checked = [&](int pg, int i) {
+    if (token_of(i) >= run.stop) return -1;
     if ((unsigned)pg < (unsigned)p.num_pages) return pg;
-    if (pg != kNoToken) atomicOr(p.err, kErrPage);
+    atomicOr(p.err, kErrPage);
     return -1;
   };
   auto fetch_first = [&]() {
     cur = fetch(lane);
-    nxt = run.g1 - run.g0 > 32 ? fetch(32 + lane) : kNoToken;
+    nxt = fetch(32 + lane);
   };
   // Step s of the piece into stage st; always one commit group a step.  What
   // is no token of the piece becomes zeros, and its page's scales too.
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     const int i0 = s * C::NS;
     if (i0 < run.g1 - run.g0) {
       if (i0 && (i0 & 31) == 0) {
-        cur = checked(nxt);
+        cur = checked(nxt, i0 + lane);
         nxt = fetch(i0 + 32 + lane);
       }
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     const uint8_t *q = (const uint8_t *)(p.q + (((long long)run.b * p.Hkv + run.h) * p.R + run.r0) * D);
     for (int i = threadIdx.x; i < rows * 2 * C::CH; i += kWarps * 32)   // a head's R rows lie together
       cp_async16<0>(sbase + C::OFF_Q + i / (2 * C::CH) * C::QROW + i % (2 * C::CH) * 16, q + i * 16);
-    cur = checked(cur);
+    cur = checked(cur, lane);
 #pragma unroll
     for (int k = 0; k < C::AHEAD; ++k) issue(k, (st + k) % kStages);
     if (threadIdx.x == 0) (void)checked_len(p.lens, run.b, p.max_pages, 1 << p.page_log2, p.err);

@@ -219,17 +219,17 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       // (Page numbers are fetched a block before they are looked at, scales a
       // block before they are used, so that no load is waited for.)
       constexpr uint32_t kNone = 0xFFFFFFFFu;
-      constexpr int kNoToken = -2147483647 - 1;
+      auto token_of = [&](int j) { return lane >= 8 || j >= n ? run.len : (run.g0 + j) * BN + lane * 16; };
       auto fetch = [&](int j) {
-        const int tok = (run.g0 + j) * BN + lane * 16;
-        return lane >= 8 || j >= n || tok >= run.len ? kNoToken : tab[tok >> p.page_log2];
+        const int tok = token_of(j);
+        return tok >= run.len ? 0 : tab[tok >> p.page_log2];
       };
       auto row_of = [&](int pg, int j) {
-        if ((unsigned)pg < (unsigned)p.num_pages) {
-          const int tok = (run.g0 + j) * BN + lane * 16;
+        const int tok = token_of(j);
+        if (tok >= run.len) return kNone;
+        if ((unsigned)pg < (unsigned)p.num_pages)
           return (((uint32_t)pg * p.Hkv + run.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1));
-        }
-        if (pg != kNoToken) atomicOr(p.err, kErrPage);
+        atomicOr(p.err, kErrPage);
         return kNone;
       };
       // this thread's chunks of K or V of block j, whose groups lie at `rows`

@@ -517,6 +517,22 @@ def test_attention_leaves_out_what_is_out_of_range(Nq):
     compare_attention(o, lse, q, cache, table, cut, 16, True, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("Nq", [1, 60])
+@pytest.mark.parametrize("page_number", [-2 ** 31, 2 ** 31 - 1, 5])
+def test_attention_reports_each_page_that_is_none(Nq, page_number):
+    """Whatever the number outside [0, num_pages), alone in its table, line or whole units."""
+    for more in (0, 60):
+        cache, table = attention_case(1, 1, 64, 16, [60], 10)
+        assert len(cache[0]) == 6
+        table[0, 2] = page_number
+        table = torch.cat([table, torch.full((1, more), -1, dtype=torch.int32)], dim=1)
+        q = torch.randn(1, 2, Nq, 64, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+        o, lse = F.forward_cache(q.cuda(), *cache, table.cuda(), i32([60]))
+        assert F.fa_device_status() == (F.FA_ERR_PAGE if page_number != 5 else F.FA_OK)
+        if page_number != 5:
+            compare_attention(o, lse, q, cache, table, [60], 16, True, 64 ** -0.5)
+
+
 @pytest.mark.parametrize("Nq", [1, 12, 40])
 def test_attention_nan_reaches_only_the_rows_that_see_it(Nq):
     """A NaN code of V in token t makes column c of the rows that see t NaN and no other value."""
