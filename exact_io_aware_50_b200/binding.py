@@ -339,7 +339,7 @@ def _t():
         import torch
         _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
         _F8 = (torch.float8_e4m3fn, torch.uint8)
-        _get_device = torch.cuda.current_device
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch = torch

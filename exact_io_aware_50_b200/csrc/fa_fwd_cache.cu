@@ -31,14 +31,14 @@
 // smaller ones err by at most 2^-37 of the largest weight.
 //
 // Measured on B200, a call in a graph, Hq 32, Hkv 8, d 128: 32 sequences of 2047 to
-// 16384 tokens (612 MB) 101 us = 6.0 TB/s, 92 % of a plain copy's rate, the bound of
-// long batches; one of 16384 tokens 14.4 us, of which 7 are the latency of a call's
+// 16384 tokens (612 MB) 98 us = 6.2 TB/s, 95 % of a plain copy's rate, the bound of
+// long batches; one of 16384 tokens 13.1 us, of which 7 are the latency of a call's
 // two launches, the page look-up, the first copies and the merge.  d = 256 holds O in
-// 128 registers a thread: B 8, Hq 16, Hkv 4, 16384 tokens 50 us = 5.3 TB/s.  Many
-// short sequences are bound by a unit's start and end, about 4 us of a CTA: 256 of
-// 256 tokens 45 us = 3.0 TB/s.  Looking up the next unit's pages and copying its first
-// steps before this one's last did not shorten that (2 to 5 % slower), nor did copies
-// by TMA (boxes of 2 to 8 KB, one CTA an SM: 130 us where this form took 109).
+// 128 registers a thread: B 8, Hq 16, Hkv 4, 16384 tokens 49 us = 5.5 TB/s.  Many
+// short sequences are bound by a unit's start and end, about 3.5 us of a CTA: 256 of
+// 256 tokens 39 us = 3.5 TB/s.  Copying the next unit's first steps before this one's
+// last did not shorten that (2 to 5 % slower), nor did copies by TMA (boxes of 2 to 8
+// KB, one CTA an SM: 130 us for the batch where this form then took 109).
 #include <type_traits>
 
 #include "fwd_cache.cuh"
@@ -174,7 +174,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
-template <int D>
+// HALF: eight rows a head or fewer, so that a lane's second row (g + 8) does not
+// exist and gets no work (Hq 32, Hkv 8, d 128, us a call in a graph without and with:
+// one sequence of 16384 tokens 14.6 / 13.1, 32 of 2047 to 16384 101 / 98, 1024 of 256
+// tokens 163 / 135, the last two with the changes to a unit's end made beside it).
+template <int D, bool HALF>
 __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const FwdCacheParams p) {
   using C = RowCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -267,7 +271,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     const int subs = run.g1 - run.g0, steps = (subs + C::NS - 1) / C::NS;
     const int rows = min(C::ROWS, p.R - run.r0), len = run.len, stop = run.stop;
     const int token = token_of(0);   // of this warp; its subtile i starts kGranule * i later
-    const bool two = rows > 8;       // else a lane's second row does not exist: no work for it
 
     // ---- q: A fragments of halves, each row times a power of two
     cp_async_wait<C::AHEAD - 1>();   // q came with the first step
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       const bool live = r < rows;
       row_c[e] = 0.f;
       lim[e] = 0;
-      if (e && !two) {
+      if (HALF && e) {
 #pragma unroll
         for (int c = 0; c < C::CH; ++c) qa[c][1] = qa[c][3] = 0u;
         continue;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int n = 0; n < C::NS; ++n) {
-          if (e && !two) continue;
+          if (HALF && e) continue;
           const float cf = row_c[e] * sk[n];
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[2 * n + (i >> 1)][2 * e + (i & 1)] *= cf;
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int n = 0; n < C::NS; ++n) {
-            if (e && !two) continue;
+            if (HALF && e) continue;
             const int seen = min(nv[n], lim[e] - j0[n]) - 2 * t;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         mxs[e] = mxo[e] = -INFINITY;
-        if (e && !two) continue;
+        if (HALF && e) continue;
 #pragma unroll
         for (int n = 0; n < C::NS; ++n) {
           float mx = -INFINITY;
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (e && !two) continue;
+          if (HALF && e) continue;
           float vs = mxs[e], vo = mxo[e];
           vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
           vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 1));
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       uint32_t pa[C::NS][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (e && !two) {
+        if (HALF && e) {
 #pragma unroll
           for (int n = 0; n < C::NS; ++n) pa[n][1] = pa[n][3] = 0u;
           continue;
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     // each row's log-sum-exp in this warp
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (e && !two) continue;
+      if (HALF && e) continue;
       float v = l[e];
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
-      if (e && !two) continue;
+      if (HALF && e) continue;
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
@@ -626,9 +629,10 @@ template <int D>
 int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   using C = RowCfg<D>;
   const FwdCacheParams p = fwd_cache_params(a, x);
-  auto kern = fwd_cache_rows_kernel<D>;
-  static unsigned long long allowed = 0;
-  if (!allow_smem(kern, C::SMEM, &allowed)) return 5;
+  const bool half = p.R <= C::ROWS / 2;
+  auto kern = half ? fwd_cache_rows_kernel<D, true> : fwd_cache_rows_kernel<D, false>;
+  static unsigned long long allowed[2] = {0, 0};
+  if (!allow_smem(kern, C::SMEM, &allowed[half])) return 5;
   kern<<<x.ctas, kWarps * 32, C::SMEM, a.stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return 5;
   return launch_fwd_cache_merge<D, typename C::L>(p, a.stream);
