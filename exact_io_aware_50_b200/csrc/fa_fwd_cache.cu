@@ -638,14 +638,15 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
   return launch_fwd_cache_merge<D, typename C::L>(p, a.stream);
 }
 
-// Up to three tiles of 16 rows (two at d = 256) go to the kernel of this file,
+// Up to three tiles of 16 rows (five at d = 64) go to the kernel of this file,
 // which reads the cache (L2, mostly) for each; more rows read it once for 128 of
-// them on tcgen05 (fa_fwd_cache_sm100.cu).  Measured on B200, us a call here /
-// there, B 32, 8000 tokens, 2 key/value heads: d = 64, 40 rows 52.5 / 85.5, 96 rows
-// 96.7 / 91.6; d = 128, 40 rows 74.5 / 80.6, 64 rows 95.8 / 85.6; d = 256, 32 rows
-// 96.6 / 116, 40 rows 126 / 121.
+// them on tcgen05 (fa_fwd_cache_sm100.cu).  Measured on B200, us a call in a graph here
+// / there, B 32, 8000 tokens, 2 key/value heads: d = 64, 80 rows 77.0 / 89.9, 96 rows
+// 90.2 / 90.4; d = 128, 48 rows 72.3 / 83.1, 64 rows 90.8 / 83.8; d = 256, 48 rows 123 /
+// 143; B 1, 16000 tokens, 8 heads, 48 rows at d = 256 39.7 / 46.3; B 16, 400 tokens, 8
+// heads, 80 rows at d = 64 20.8 / 17.2, 40 rows at d = 256 27.8 / 21.7.
 bool few_rows(const CacheArgs &a) {
-  return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 256 ? 2 : 3) * 16;
+  return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 64 ? 5 : 3) * 16;
 }
 
 FwdCachePlan plan_of(const CacheArgs &a) {
