@@ -51,8 +51,6 @@ constexpr int kSub = 16;                        // tokens of a subtile (one page
 constexpr int kGranule = kWarps * kSub;
 constexpr int kStage = 8 * 1024, kStages = 3;   // a warp's ring
 constexpr int kRing = kStage * kStages;
-constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
-constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 
 template <int D>
 struct RowCfg {
@@ -429,7 +427,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
           mxo[e] = fmaxf(mxo[e], mx + lsv[n]);
         }
         moved |= mxs[e] > m_s[e] + kLag || mxo[e] > m_o[e] + kLag;
+#pragma unroll
+        for (int n = 0; n < C::NS; ++n) moved |= lsv[n] - (m_o[e] - m_s[e]) > kOver - kShift;
       }
+      bool over = false;   // some weight's factor passes 2^kOver
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -451,9 +452,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
             o[n][2 * e] *= ao;
             o[n][2 * e + 1] *= ao;
           }
+#pragma unroll
+          for (int n = 0; n < C::NS; ++n) over |= lsv[n] - (m_o[e] - m_s[e]) > kOver - kShift;
         }
+        over = __any_sync(0xffffffffu, over);
       }
       uint32_t pa[C::NS][4];
+      float ms[2], diff[2];   // weight = 2^{s - ms} * 2^{diff + log2 sv}
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (HALF && e) {
@@ -462,22 +467,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
           continue;
         }
         const bool none = m_s[e] == -INFINITY;
-        const float ms = none ? 0.f : m_s[e];
-        const float diff = none ? 0.f : m_s[e] - m_o[e] + kShift;
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < C::NS; ++n) {
-          const float gain = fast_exp2(diff + lsv[n]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p0 = fast_exp2(sc[2 * n + i][2 * e] - ms);
-            const float p1 = fast_exp2(sc[2 * n + i][2 * e + 1] - ms);
-            sum += p0 + p1;
-            pa[n][2 * i + e] = pack_half2(p0 * gain, p1 * gain);
-          }
-        }
-        l[e] += sum;
+        ms[e] = none ? 0.f : m_s[e];
+        diff[e] = none ? 0.f : m_s[e] - m_o[e] + kShift;
       }
+      // sums of a row's tokens' powers, and their weights
+      auto weigh = [&](auto apart) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (HALF && e) continue;
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < C::NS; ++n) {
+            const float up = diff[e] + lsv[n], gain = fast_exp2(up);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x0 = sc[2 * n + i][2 * e] - ms[e], x1 = sc[2 * n + i][2 * e + 1] - ms[e];
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              sum += p0 + p1;
+              pa[n][2 * i + e] = apart ? pack_half2(p0 * gain, p1 * gain)
+                                       : pack_half2(fast_exp2(x0 + up), fast_exp2(x1 + up));
+            }
+          }
+          l[e] += sum;
+        }
+      };
+      if (over) weigh(std::false_type{});
+      else weigh(std::true_type{});
 
       // ---- a token that some row does not see may hold a NaN code in V, and
       // 0 * NaN is NaN: such codes become 0, and the columns of the rows that

@@ -48,8 +48,6 @@ constexpr int kThreads = 512;
 // 512 of 512 119.6 / 65.8.  With a unit for every CTA, B 8, 512 of 2048 238 / 198 (ragged
 // 207 / 177), 512 of 4096 387 / 368 (ragged 277 / 328).
 constexpr int kWhole = 512, kWholeMany = 2048;
-constexpr float kLag = 3.f;                     // a maximum may lag by 2^3
-constexpr float kShift = 12.f;                  // weights are stored times 2^12: at most 2^15
 constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
 
 template <int D_, int NT_>
@@ -71,7 +69,8 @@ struct TileCfg {
   static constexpr int OFF_K = OFF_P + NT * P_TILE;
   static constexpr int OFF_V = OFF_K + TILE;
   static constexpr int OFF_SCALE = OFF_V + TILE;             // [4][8] (sk, log2 sv) of a block's 16-token groups
-  static constexpr int OFF_NAN = OFF_SCALE + 4 * 8 * 8;      // [2][D] first NaN token of a column
+  static constexpr int OFF_PAGES = OFF_SCALE + 4 * 8 * 8;    // [4] Pages of a block
+  static constexpr int OFF_NAN = OFF_PAGES + 4 * 8;          // [2][D] first NaN token of a column
   static constexpr int OFF_ANY = OFF_NAN + 2 * D * 4;        // [2] whether there is one
   static constexpr int OFF_PIECE = OFF_ANY + 8;              // [2] Piece
   static constexpr int OFF_BAR = OFF_PIECE + 2 * 32;
@@ -88,6 +87,15 @@ struct Piece {
   int b, h, r0, blocks, token, len, part, unused;
 };
 static_assert(sizeof(Piece) == 32, "Piece");
+
+// What the converters say of a block's pages: whether some group has none; the
+// largest log2 sv of the block, where the piece's so far differ by so much that a
+// weight's factor may pass 2^kOver (up is at most kShift + their difference), else -inf.
+struct Pages {
+  int hole;
+  float top;
+};
+static_assert(sizeof(Pages) == 8, "Pages");
 
 // D[tmem] (+)= A B with halves: the format fields 0.
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -110,6 +118,14 @@ __device__ __forceinline__ void store_halves(uint32_t at, const uint4 &codes) {
   }
   st_shared_v4(at, h[0], h[1], h[2], h[3]);
   st_shared_v4(at ^ 16, h[4], h[5], h[6], h[7]);
+}
+
+// The largest of each N neighbouring lanes' values.
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int off = N / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
 }
 
 // 32 bytes, a whole sector, in one store.
@@ -136,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE);
+  Pages *block_pages = reinterpret_cast<Pages *>(smem + C::OFF_PAGES);
   // Two lists of NaN codes, for pieces in turn.  A piece's converters clear the
   // next piece's list before they hand over their last V.
   int *nan_at = reinterpret_cast<int *>(smem + C::OFF_NAN), *nan_any = reinterpret_cast<int *>(smem + C::OFF_ANY);
@@ -268,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       load(p.k_cache, 0, row0, kr);
       load(p.v_cache, 0, row0, vr);
       float2 sc = scale_of(row0);
+      float lo = INFINITY, hi = -INFINITY;   // log2 sv of the piece's pages so far
 
       // tokens that every row of the piece sees
       const int lim_min = p.causal ? max(0, min(run.len, run.len - p.Nq + run.r0 / p.g + 1)) : run.len;
@@ -277,7 +295,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         if (j < n) {
           ok = warp_wait_all(bar(B_KEMPTY), ((g + j) & 1) ^ 1, wc);
           if (!ok) break;
-          if (ct < 8) scales[((g + j) & 3) * 8 + ct] = make_float2(sc.x, log2f(sc.y));
+          if (warp == C::SOFT) {
+            const float lsv = log2f(sc.y);
+            if (lane < 8) scales[((g + j) & 3) * 8 + lane] = make_float2(sc.x, lsv);
+            const unsigned there = __ballot_sync(0xffffffffu, lsv != -INFINITY);   // lanes 8 and up: none
+            const float top = group_max<8>(lsv);
+            hi = fmaxf(hi, top);
+            lo = fminf(lo, -group_max<8>(lsv != -INFINITY ? -lsv : -INFINITY));
+            if (leader) block_pages[(g + j) & 3] = Pages{(there & 0xFFu) != 0xFFu, hi - lo > kOver - kShift ? top : -INFINITY};
+          }
           store(C::OFF_K, kr);
           fence_proxy_async_smem();
           mbar_arrive(bar(B_KFULL));
@@ -487,9 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         const int col0 = x.token + j * BN;
         uint32_t sr[64];
         float *s = reinterpret_cast<float *>(sr);
-        bool whole = col0 + BN <= lim_warp;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) whole = whole && scs[q].y != -INFINITY;
+        const Pages pages = block_pages[(g + j) & 3];
+        const bool whole = col0 + BN <= lim_warp && !pages.hole;
         auto read_half = [&](int h) {
           tmem_ld32(ts + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
           tmem_ld32(ts + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
@@ -533,16 +558,41 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         const bool none = m_s == -INFINITY;
         const float ms = none ? 0.f : m_s, diff = none ? 0.f : m_s - m_o + kShift;
         float sum = 0.f;
+        if (g + j > 0) {                      // P V of the block before is done with P
+          ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
+          tc_fence_after();
+          if (!ok) break;
+        }
+        const bool over = __any_sync(0xffffffffu, diff + pages.top > kOver);
+        if (over) {                           // 16 columns at a time, small rather than fast
 #pragma unroll 1
-        for (int h = 1; h >= 0; --h) {
+          for (int q = 0; q < 8; ++q) {
+            const float2 kv = scs[q];
+            const float cf = fmaxf(rc * kv.x, kTiny), up = diff + kv.y;
+            const int seen = kv.y == -INFINITY ? 0 : lim - col0 - 16 * q;
+            uint32_t sq[16], pk[8];
+            tmem_ld16(ts + 16 * q, sq);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float x0 = e < seen ? fmaf(__uint_as_float(sq[e]), cf, -ms) : -INFINITY;
+              const float x1 = e + 1 < seen ? fmaf(__uint_as_float(sq[e + 1]), cf, -ms) : -INFINITY;
+              sum += fast_exp2(x0) + fast_exp2(x1);
+              pk[e / 2] = pack_half2(fast_exp2(x0 + up), fast_exp2(x1 + up));
+            }
+            const uint32_t at = prow + (q >> 2) * C::CHUNK + (((2 * (q & 3)) ^ (r & 7)) << 4);
+            st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
+            st_shared_v4(at ^ 16, pk[4], pk[5], pk[6], pk[7]);
+          }
+          tc_fence_before();
+          mbar_arrive(bar(B_SEMPTY + t));
+        }
+#pragma unroll 1
+        for (int h = over ? -1 : 1; h >= 0; --h) {
           if (h == 0) {
             read_half(0);
             tc_fence_before();
             mbar_arrive(bar(B_SEMPTY + t));   // the next block's S may take the columns
-          } else if (g + j > 0) {             // P V of the block before is done with P
-            ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
-            tc_fence_after();
-            if (!ok) break;
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -566,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           }
         }
         l = l * al + sum;
-        if (!ok) break;
         fence_proxy_async_smem();
         if (rescale && j > 0) {
 #pragma unroll 1

@@ -18,6 +18,15 @@ __device__ __forceinline__ void wait_for_primary() {
 }
 
 constexpr int kMaxCtas = 2 * 148;   // CTAs of a launch, at most
+constexpr float kLag = 3.f;         // a maximum may lag by 2^3
+constexpr float kShift = 12.f;      // weights are stored times 2^12: at most 2^15
+// A weight 2^{s - m} * 2^up, up = m - M + kShift + log2 sv, is the product of its two
+// powers where up is at most this (the second is the same for a page's tokens), and
+// one power of the exponents' sum where it is more: there 2^up nears float32's end,
+// and infinity times the 0 of a hidden or distant token is NaN.  Up to 2^100, a first
+// power that is flushed to 0 (below 2^-126) stands for less than 2^-26, which is 0 as
+// a half.  Pages of zeros make up large: their scale is 2^-112.
+constexpr float kOver = 100.f;
 
 struct FwdCacheParams {
   const __nv_bfloat16 *q;

@@ -1,0 +1,84 @@
+"""Attention over the paged E4M3 cache at the ends of its range: pages whose V has
+very different scales, hidden ones among them.
+
+Tolerances are those of test_gpu_serving.py (a weight rounded once to 11 bits, the
+scores' error e_s through the exponential, float32 sums, weights below 2^-26 of a row's
+largest to steps of it, half a step of the output) plus what tiny results add: half
+a step of bfloat16's subnormals, 2^-134, and float32's in the partial results and their
+products, less than 2^-140 in all.
+"""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_50_b200 as F
+from oracle import serving as S
+from test_gpu_serving import U16, f64, i32, new_cache, np_cache
+
+pytestmark = pytest.mark.gpu
+TINY = 2.0 ** -134 + 2.0 ** -140
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    F.lib()
+    yield
+
+
+def cache_of(k, v, lens, page, wide=0):
+    """Sequences' tokens k, v [B, H, n, d] (float32) in a cache whose pages stand in
+    no order and whose free slots hold NaN codes; the table has room for `wide` more
+    tokens, on pages that are none."""
+    B, H, n, d = k.shape
+    width = (n + page - 1) // page
+    cache = new_cache(B * width + 1, H, page, d)
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(n)).reshape(B, width).to(torch.int32)
+    F.cache_append(k.cuda(), v.cuda(), *cache, table.cuda(), i32([0] * B), i32(lens))
+    return cache, torch.cat([table, torch.full((B, wide // page), -1, dtype=torch.int32)], dim=1)
+
+
+def check(q, cache, table, lens, page, causal, scale):
+    o, lse = F.forward_cache(q.cuda(), *cache, table.cuda(), i32(lens), scale=scale, causal=causal)
+    torch.cuda.synchronize()
+    assert F.fa_device_status() == F.FA_OK
+    ref_o, ref_l, w, amp, unit = S.cache_attention(f64(q), *np_cache(cache), table.tolist(), lens, page, scale, causal)
+    o, lse, d = f64(o), f64(lse), q.shape[3]
+    none = np.isneginf(ref_l)
+    assert np.array_equal(np.isneginf(lse), none) and (o[none] == 0).all()
+    e_s = amp * (d * 2.0 ** -23 + 2.0 ** -20)
+    assert e_s.max() < 0.1
+    tol = np.abs(ref_o) * U16 + w * (2.0 ** -11 + 2.0 ** -13 + np.expm1(2 * e_s[..., None])) + unit * 2.0 ** -37 + TINY
+    bad = np.abs(o - ref_o) - tol
+    at = np.unravel_index(np.argmax(np.where(np.isfinite(bad), bad, np.inf)), bad.shape)
+    assert np.isfinite(o).all() and (bad <= 0).all(), f"O[{at}] = {o[at]:.6g}, not {ref_o[at]:.6g} within {tol[at]:.3g}"
+    lse, ref_l, e_s = lse[~none], ref_l[~none], e_s[~none]
+    assert (np.abs(lse - ref_l) <= e_s + 2.0 ** -18 * (1 + np.abs(ref_l))).all()
+
+
+ROWS = [(1, 1), (4, 5), (1, 130)]    # query heads, queries: one row, two 16-row tiles, 128-row tiles
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("gap,first,others", [
+    (80, 0, 8000), (80, 0, 1e20), (20, 0, 1e30), (80, 1e-25, 1e10), (-80, 1e20, 0), (-80, 1e10, 1e-25)])
+def test_v_scales_far_apart(gap, first, others, d, rows):
+    """The first page's keys score `gap` nats above the others; its V is of size
+    `first`, the others' of size `others`.  Early causal queries see the first
+    page alone, with the others hidden beside it."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(d + Nq)
+    lens, page = [66, 140, 200], 16
+    k, v = torch.randn(2, 3, 1, 200, d, generator=g)
+    k[..., 0] = 0
+    k[:, :, :page] = 0
+    k[:, :, :page, 0] = gap
+    v[:, :, :page] *= first
+    v[:, :, page:] *= others
+    q = 0.1 * torch.randn(3, Hq, Nq, d, generator=g)
+    q[..., 0] = 1.0
+    for wide in (0, 4096):
+        cache, table = cache_of(k, v, lens, page, wide)
+        check(q.to(torch.bfloat16), cache, table, lens, page, True, 1.0)
