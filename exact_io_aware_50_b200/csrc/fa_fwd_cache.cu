@@ -325,15 +325,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     }
 
     float o[D / 8][4];
-    float m_s[2], m_o[2], l[2];
+    float m_s[2], m_d[2], l[2];   // m, M - m, sum of 2^{s - m}
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m_s[e] = m_o[e] = -INFINITY;
-      l[e] = 0.f;
+      m_s[e] = -INFINITY;
+      m_d[e] = l[e] = 0.f;
     }
 
 #pragma unroll 1
@@ -398,7 +398,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
           if (HALF && e) continue;
           const float cf = row_c[e] * sk[n];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[2 * n + (i >> 1)][2 * e + (i & 1)] *= cf;
+          for (int i = 0; i < 4; ++i) {
+            float &x = sc[2 * n + (i >> 1)][2 * e + (i & 1)];
+            x = __fmul_rn(x, cf);   // rounded before m is subtracted: equal scores, equal powers
+          }
         }
       if (!whole) {
 #pragma unroll
@@ -412,40 +415,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
               if (8 * (i >> 1) + (i & 1) >= seen) sc[2 * n + (i >> 1)][2 * e + (i & 1)] = -INFINITY;
           }
       }
-      bool moved = false;
-      float mxs[2], mxo[2];   // row maxima of s and of s + log2 sv
+      // Scores may be of any size, so they are compared by their differences, which
+      // are exact where they are small.
+      bool moved = false, over = false;   // over: some weight's factor passes 2^kOver
+      float mx[2][C::NS];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mxs[e] = mxo[e] = -INFINITY;
         if (HALF && e) continue;
+        float mxs = -INFINITY, mxo = -INFINITY;   // of s, of s - m + log2 sv
 #pragma unroll
         for (int n = 0; n < C::NS; ++n) {
-          float mx = -INFINITY;
+          float v = sc[2 * n][2 * e];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sc[2 * n + (i >> 1)][2 * e + (i & 1)]);
-          mxs[e] = fmaxf(mxs[e], mx);
-          mxo[e] = fmaxf(mxo[e], mx + lsv[n]);
+          for (int i = 1; i < 4; ++i) v = fmaxf(v, sc[2 * n + (i >> 1)][2 * e + (i & 1)]);
+          mx[e][n] = v;
+          mxs = fmaxf(mxs, v);
+          mxo = fmaxf(mxo, v - m_s[e] + lsv[n]);   // infinite for a row's first keys
+          moved |= lsv[n] - m_d[e] > kOver - kShift;
         }
-        moved |= mxs[e] > m_s[e] + kLag || mxo[e] > m_o[e] + kLag;
-#pragma unroll
-        for (int n = 0; n < C::NS; ++n) moved |= lsv[n] - (m_o[e] - m_s[e]) > kOver - kShift;
+        moved |= mxs - m_s[e] > kLag || mxo > m_d[e] + kLag;
       }
-      bool over = false;   // some weight's factor passes 2^kOver
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           if (HALF && e) continue;
-          float vs = mxs[e], vo = mxo[e];
-          vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
-          vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 1));
-          vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 2));
-          vo = fmaxf(vo, __shfl_xor_sync(0xffffffffu, vo, 2));
-          const float ns = fmaxf(m_s[e], vs), no = fmaxf(m_o[e], vo);
+          float ns = m_s[e];
+#pragma unroll
+          for (int n = 0; n < C::NS; ++n) ns = fmaxf(ns, mx[e][n]);
+          ns = fmaxf(ns, __shfl_xor_sync(0xffffffffu, ns, 1));
+          ns = fmaxf(ns, __shfl_xor_sync(0xffffffffu, ns, 2));
           // a row that has seen no key yet has l = 0 and O = 0
-          const float al = ns == m_s[e] ? 1.f : fast_exp2(m_s[e] - ns);
-          const float ao = no == m_o[e] ? 1.f : fast_exp2(m_o[e] - no);
+          const float shift = ns == m_s[e] ? 0.f : m_s[e] - ns;
+          float nd = shift + m_d[e];
+#pragma unroll
+          for (int n = 0; n < C::NS; ++n) nd = fmaxf(nd, mx[e][n] - ns + lsv[n]);
+          nd = fmaxf(nd, __shfl_xor_sync(0xffffffffu, nd, 1));
+          nd = fmaxf(nd, __shfl_xor_sync(0xffffffffu, nd, 2));
+          const float al = fast_exp2(shift), ao = fast_exp2(shift + (m_d[e] - nd));   // 1 where nothing moved
           m_s[e] = ns;
-          m_o[e] = no;
+          m_d[e] = nd;
           l[e] *= al;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) {
@@ -453,12 +461,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
             o[n][2 * e + 1] *= ao;
           }
 #pragma unroll
-          for (int n = 0; n < C::NS; ++n) over |= lsv[n] - (m_o[e] - m_s[e]) > kOver - kShift;
+          for (int n = 0; n < C::NS; ++n) over |= lsv[n] - nd > kOver - kShift;
         }
         over = __any_sync(0xffffffffu, over);
       }
       uint32_t pa[C::NS][4];
-      float ms[2], diff[2];   // weight = 2^{s - ms} * 2^{diff + log2 sv}
+      float ms[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (HALF && e) {
@@ -466,9 +474,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
           for (int n = 0; n < C::NS; ++n) pa[n][1] = pa[n][3] = 0u;
           continue;
         }
-        const bool none = m_s[e] == -INFINITY;
-        ms[e] = none ? 0.f : m_s[e];
-        diff[e] = none ? 0.f : m_s[e] - m_o[e] + kShift;
+        ms[e] = m_s[e] == -INFINITY ? 0.f : m_s[e];
       }
       // sums of a row's tokens' powers, and their weights
       auto weigh = [&](auto apart) {
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < C::NS; ++n) {
-            const float up = diff[e] + lsv[n], gain = fast_exp2(up);
+            const float up = kShift - m_d[e] + lsv[n], gain = fast_exp2(up);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float x0 = sc[2 * n + i][2 * e] - ms[e], x1 = sc[2 * n + i][2 * e + 1] - ms[e];
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       for (int w = 0; w < kWarps; ++w)
         sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
       f[e] = l[e] == 0.f ? 0.f
-                         : fast_exp2(m_o[e] - kShift - m_s[e]) / l[e] *
+                         : fast_exp2(m_d[e] - kShift) / l[e] *
                                (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
       if (warp == 0 && t == 0 && r < rows) {
         const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);

@@ -48,6 +48,7 @@ constexpr int kThreads = 512;
 // 512 of 512 119.6 / 65.8.  With a unit for every CTA, B 8, 512 of 2048 238 / 198 (ragged
 // 207 / 177), 512 of 4096 387 / 368 (ragged 277 / 328).
 constexpr int kWhole = 512, kWholeMany = 2048;
+constexpr float kBig = 1048576.f;               // scores past this are not subtracted in one rounding (half an ulp is 2^-4)
 constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
 
 template <int D_, int NT_>
@@ -452,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       const int lim = !live ? x.len : (p.causal ? max(0, min(x.len, x.len - p.Nq + i + 1)) : x.len);
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
       const long long row = ((long long)x.b * p.Hq + hq) * p.Nq + i;   // of q, o, lse
-      float m_s = -INFINITY, m_o = -INFINITY, l = 0.f;
+      float m_s = -INFINITY, m_d = -INFINITY, l = 0.f;   // m, M - m, sum of 2^{s - m}
+      bool big = false;   // some row's m is past kBig
 
       // ---- q: the warp converts its 32 rows (D / 8 lanes a row), each times a
       // power of two that brings its largest entry to [2^13, 2^14).  The tile is
@@ -528,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
             }
           }
         };
-        // row maxima of s (base 2) and of s + log2 sv, by the pages' groups
+        // row maxima of s - m (base 2; of s for the first keys), by the pages' groups,
+        // and of s - m + log2 sv
+        const float m_0 = m_s == -INFINITY ? 0.f : m_s;
         float mxs = -INFINITY, mxo = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -539,24 +543,50 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
             float mx = s[16 * q];
 #pragma unroll
             for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[16 * q + e]);
-            mx *= fmaxf(rc * kv.x, kTiny);
+            mx = fmaf(mx, fmaxf(rc * kv.x, kTiny), -m_0);
             mxs = fmaxf(mxs, mx);
             mxo = fmaxf(mxo, mx + kv.y);
           }
         }
-        const bool moved = mxs > m_s + kLag || mxo > m_o + kLag;
         float al = 1.f, ao = 1.f;
-        const bool rescale = __any_sync(0xffffffffu, moved);
+        const bool rescale = __any_sync(0xffffffffu, mxs > kLag || mxo > m_d + kLag) || big;
         if (rescale) {
-          const float ns = fmaxf(m_s, mxs), no = fmaxf(m_o, mxo);
+          float ns = m_s == -INFINITY ? mxs : m_s + fmaxf(mxs, 0.f), top = mxo - (ns - m_0);
+          big = __any_sync(0xffffffffu, fabsf(m_0) > kBig || (fabsf(ns) > kBig && ns != -INFINITY));
+          if (big) {
+            // Scores so large that s - m above is off by whole units: s rounded once, by
+            // which equal scores stay equal, and exact differences.  The best of s +
+            // log2 sv is kept as its two parts.
+            float best_s = -INFINITY, best_v = 0.f;
+            ns = m_s;
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+              const float2 kv = scs[q];
+              const int seen = kv.y == -INFINITY ? 0 : lim - col0 - 16 * q;
+              uint32_t sq[16];
+              tmem_ld16(ts + 16 * q, sq);
+              tmem_wait_ld();
+              float mx = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) mx = fmaxf(mx, e < seen ? __uint_as_float(sq[e]) : -INFINITY);
+              mx = __fmul_rn(mx, fmaxf(rc * kv.x, kTiny));
+              ns = fmaxf(ns, mx);
+              if (mx - best_s + (kv.y - best_v) > 0.f) {
+                best_s = mx;
+                best_v = kv.y;
+              }
+            }
+            top = best_s - ns + best_v;
+          }
           // a row that has seen no key yet has l = 0 and O = 0 (or nothing, block 0)
-          al = ns == m_s ? 1.f : fast_exp2(m_s - ns);
-          ao = no == m_o ? 1.f : fast_exp2(m_o - no);
+          const float shift = ns == m_s ? 0.f : m_s - ns, nd = fmaxf(shift + m_d, top);
+          al = fast_exp2(shift);
+          ao = nd == m_d ? al : fast_exp2(shift + (m_d - nd));
           m_s = ns;
-          m_o = no;
+          m_d = nd;
         }
         const bool none = m_s == -INFINITY;
-        const float ms = none ? 0.f : m_s, diff = none ? 0.f : m_s - m_o + kShift;
+        const float ms = none ? 0.f : m_s, diff = none ? 0.f : kShift - m_d;
         float sum = 0.f;
         if (g + j > 0) {                      // P V of the block before is done with P
           ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
@@ -637,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       // ------------------------------------------------------------ epilogue
       tc_fence_after();
       const bool seen = !(l == 0.f);
-      const float f = seen ? fast_exp2(m_o - kShift - m_s) / l : 0.f;
+      const float f = seen ? fast_exp2(m_d - kShift) / l : 0.f;
       const bool nans = nan_any[u & 1] != 0;
       const long long prt = x.part < 0 ? 0 : (long long)(x.part + t * BM + r);
 #pragma unroll 1

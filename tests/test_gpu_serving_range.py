@@ -1,5 +1,5 @@
 """Attention over the paged E4M3 cache at the ends of its range: pages whose V has
-very different scales, hidden ones among them.
+very different scales, hidden ones among them; scores of any size.
 
 Tolerances are those of test_gpu_serving.py (a weight rounded once to 11 bits, the
 scores' error e_s through the exponential, float32 sums, weights below 2^-26 of a row's
@@ -13,6 +13,7 @@ import torch
 
 import exact_io_aware_50_b200 as F
 from oracle import serving as S
+from oracle.fp8 import e4m3_decode
 from test_gpu_serving import U16, f64, i32, new_cache, np_cache
 
 pytestmark = pytest.mark.gpu
@@ -39,8 +40,10 @@ def cache_of(k, v, lens, page, wide=0):
     return cache, torch.cat([table, torch.full((B, wide // page), -1, dtype=torch.int32)], dim=1)
 
 
-def check(q, cache, table, lens, page, causal, scale):
-    o, lse = F.forward_cache(q.cuda(), *cache, table.cuda(), i32(lens), scale=scale, causal=causal)
+def check(q, cache, table, lens, page, causal, scale, exact_scores=False):
+    """exact_scores: the scores' differences are 0 or many times their error, so that the
+    error of a score does not enter O."""
+    out = o, lse = F.forward_cache(q.cuda(), *cache, table.cuda(), i32(lens), scale=scale, causal=causal)
     torch.cuda.synchronize()
     assert F.fa_device_status() == F.FA_OK
     ref_o, ref_l, w, amp, unit = S.cache_attention(f64(q), *np_cache(cache), table.tolist(), lens, page, scale, causal)
@@ -48,13 +51,15 @@ def check(q, cache, table, lens, page, causal, scale):
     none = np.isneginf(ref_l)
     assert np.array_equal(np.isneginf(lse), none) and (o[none] == 0).all()
     e_s = amp * (d * 2.0 ** -23 + 2.0 ** -20)
-    assert e_s.max() < 0.1
-    tol = np.abs(ref_o) * U16 + w * (2.0 ** -11 + 2.0 ** -13 + np.expm1(2 * e_s[..., None])) + unit * 2.0 ** -37 + TINY
+    e_o = 0 * e_s if exact_scores else e_s
+    assert e_o.max() < 0.1
+    tol = np.abs(ref_o) * U16 + w * (2.0 ** -11 + 2.0 ** -13 + np.expm1(2 * e_o[..., None])) + unit * 2.0 ** -37 + TINY
     bad = np.abs(o - ref_o) - tol
     at = np.unravel_index(np.argmax(np.where(np.isfinite(bad), bad, np.inf)), bad.shape)
     assert np.isfinite(o).all() and (bad <= 0).all(), f"O[{at}] = {o[at]:.6g}, not {ref_o[at]:.6g} within {tol[at]:.3g}"
     lse, ref_l, e_s = lse[~none], ref_l[~none], e_s[~none]
     assert (np.abs(lse - ref_l) <= e_s + 2.0 ** -18 * (1 + np.abs(ref_l))).all()
+    return out
 
 
 ROWS = [(1, 1), (4, 5), (1, 130)]    # query heads, queries: one row, two 16-row tiles, 128-row tiles
@@ -82,3 +87,34 @@ def test_v_scales_far_apart(gap, first, others, d, rows):
     for wide in (0, 4096):
         cache, table = cache_of(k, v, lens, page, wide)
         check(q.to(torch.bfloat16), cache, table, lens, page, True, 1.0)
+
+
+SIZES = [1e3, 1e5, 1e6, 3e6, 1.2e7, 4e7, 1e8, 2.5e8, 1e9, 1e12, 1e30]
+
+
+def large_scores(size, B, Hq, Nq, d, g):
+    """q whose product with a key (1, 0, ..) is about +-size / 0.7, no two rows alike."""
+    q = torch.randn(B, Hq, Nq, d, generator=g)
+    q[..., 0] = (1 + torch.rand(B, Hq, Nq, generator=g)) * size * torch.tensor([1.0, -1.0])[torch.arange(Nq) % 2]
+    return q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", ROWS[:2], ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("size", SIZES)
+def test_equal_keys_of_large_scores(size, d, rows):
+    """Equal scores, however large, share the weight equally, whatever the pages' scales:
+    a row that sees one key returns its V."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(d + Nq)
+    lens, page = [1, 64, 256], 16
+    k = torch.zeros(3, 1, 256, d)
+    k[..., 0] = 1.0
+    v = torch.randn(3, 1, 256, d, generator=g)
+    for b, f in enumerate((1.0, 2.0 ** 9, 2.0 ** -14)):
+        v[b].view(16, page, d)[b::3] *= f
+    cache, table = cache_of(k, v, lens, page)
+    q = large_scores(size, 3, Hq, Nq, d, g)
+    o, _ = check(q, cache, table, lens, page, False, 0.7, exact_scores=True)
+    one = e4m3_decode(cache[1][int(table[0, 0]), 0, 0].cpu().numpy()) * float(cache[3][int(table[0, 0]), 0])
+    assert (f64(o[0]) == one).all()
