@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           tc_fence_after();
           if (!ok) break;
         }
-        const bool over = __any_sync(0xffffffffu, diff + pages.top > kOver);
-        if (over) {                           // 16 columns at a time, small rather than fast
+        const bool apart = __any_sync(0xffffffffu, diff + pages.top > kOver) || big;
+        if (apart) {                          // 16 columns at a time, small rather than fast
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
             const float2 kv = scs[q];
@@ -605,8 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float x0 = e < seen ? fmaf(__uint_as_float(sq[e]), cf, -ms) : -INFINITY;
-              const float x1 = e + 1 < seen ? fmaf(__uint_as_float(sq[e + 1]), cf, -ms) : -INFINITY;
+              // s rounded before m is subtracted: the largest gives 0, equal ones the same
+              const float x0 = e < seen ? __fmul_rn(__uint_as_float(sq[e]), cf) - ms : -INFINITY;
+              const float x1 = e + 1 < seen ? __fmul_rn(__uint_as_float(sq[e + 1]), cf) - ms : -INFINITY;
               sum += fast_exp2(x0) + fast_exp2(x1);
               pk[e / 2] = pack_half2(fast_exp2(x0 + up), fast_exp2(x1 + up));
             }
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           mbar_arrive(bar(B_SEMPTY + t));
         }
 #pragma unroll 1
-        for (int h = over ? -1 : 1; h >= 0; --h) {
+        for (int h = apart ? -1 : 1; h >= 0; --h) {
           if (h == 0) {
             read_half(0);
             tc_fence_before();

@@ -99,7 +99,7 @@ def large_scores(size, B, Hq, Nq, d, g):
     return q.to(torch.bfloat16)
 
 
-@pytest.mark.parametrize("rows", ROWS[:2], ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("size", SIZES)
 def test_equal_keys_of_large_scores(size, d, rows):
@@ -118,3 +118,23 @@ def test_equal_keys_of_large_scores(size, d, rows):
     o, _ = check(q, cache, table, lens, page, False, 0.7, exact_scores=True)
     one = e4m3_decode(cache[1][int(table[0, 0]), 0, 0].cpu().numpy()) * float(cache[3][int(table[0, 0]), 0])
     assert (f64(o[0]) == one).all()
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("size", SIZES)
+def test_one_key_above_the_others(size, rows):
+    """The largest of several scores, all large, takes the whole weight; one block may
+    raise the maximum by any amount, and V's scales differ by up to 2^40."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(Nq)
+    lens, page, d = [500, 333, 190], 32, 64
+    k = torch.zeros(3, 1, 500, d)
+    k[..., 0] = (torch.rand(3, 1, 500, generator=g) - 0.5) * torch.logspace(-6, 0, 500)[None, None, :]
+    k[:, 0, 7, 0], k[:, 0, 401, 0], k[:, 0, 150, 0], k[:, 0, 155, 0] = 1.5, 2.0, -1.5, -2.0
+    k[2, 0, 20] *= 0
+    v = torch.randn(3, 1, 500, d, generator=g)
+    v[..., 64:96, :] *= 2.0 ** 20
+    v[..., 384:416, :] *= 2.0 ** -20
+    for wide in (0, 4096):
+        cache, table = cache_of(k, v, lens, page, wide)
+        check(large_scores(max(size, 1e4), 3, Hq, Nq, d, g), cache, table, lens, page, False, 0.7, exact_scores=True)
