@@ -12,9 +12,10 @@
 // among the CTAs (two per SM), so ragged lengths, few heads and long caches all
 // fill the GPU: a CTA's run may start inside one unit and end inside another.
 // A unit that one CTA covers is finished there; the others leave their
-// normalised partial O and log-sum-exp in the workspace, and the merge kernel
-// joins them (L = log sum 2^{L_c}, O = sum 2^{L_c - L} O_c).  Nothing is
-// accumulated by atomics: results do not depend on timing.
+// normalised partial O, m and l in the workspace, and the merge kernel joins them
+// (m = max m_c, l = sum 2^{m_c - m} l_c, O = sum 2^{m_c - m} l_c O_c / l; not by m +
+// log2 l, which large scores round by more than l matters).  Nothing is accumulated
+// by atomics: results do not depend on timing.
 //
 // Each of a CTA's four warps takes 16 tokens of a granule, NS granules a step,
 // into a ring of its own (three stages of 8 KB) by 16-byte asynchronous copies,
@@ -83,8 +84,8 @@ struct RowCfg {
   static constexpr bool QS = D == 256;
   static constexpr int OFF_QF = OFF_Q + ROWS * QROW;
   static constexpr int OFF_SCALE = OFF_QF + (QS ? CH * 512 : 0);         // [warp][stage][NS] (sk, sv)
-  static constexpr int OFF_STAT = OFF_SCALE + kWarps * kStages * NS * 8; // [warp][ROWS]
-  static constexpr int SMEM = OFF_STAT + kWarps * ROWS * 4;
+  static constexpr int OFF_STAT = OFF_SCALE + kWarps * kStages * NS * 8; // [warp][ROWS] (m, l)
+  static constexpr int SMEM = OFF_STAT + kWarps * ROWS * 8;
   static_assert(2 * NS * TILE == kStage, "K and V codes of a step");
   static_assert(ROWS * JOIN * 4 <= kStage, "a warp's O fits beside the copies ahead");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 
   const uint32_t sbase = smem_u32(smem), ring = sbase + warp * kRing;
   float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SCALE) + warp * kStages * C::NS;
-  float *stat = reinterpret_cast<float *>(smem + C::OFF_STAT);   // [warp][ROWS]
+  float2 *stat = reinterpret_cast<float2 *>(smem + C::OFF_STAT);   // [warp][ROWS]
   const uint32_t copy_dst = tile_at<D>(lane / C::CH, lane % C::CH);
   // this lane's row and chunk of a tile's first ldmatrix of K and of V
   const uint32_t k_off = tile_at<D>(lane & 7, lane >> 3), v_off = tile_at<D>(lane & 15, lane >> 4);
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     const int part = run.part(p);
     const bool more = run.template next<D>(p, warp == 0);
     if (more) fetch_first();
-    // each row's log-sum-exp in this warp
+    // each row's m and l in this warp
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (HALF && e) continue;
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       v += __shfl_xor_sync(0xffffffffu, v, 2);
       l[e] = v;
-      if (t == 0) stat[warp * C::ROWS + g + 8 * e] = v == 0.f ? -INFINITY : m_s[e] + log2f(v);
+      if (t == 0) stat[warp * C::ROWS + g + 8 * e] = make_float2(m_s[e], v);
     }
     __syncthreads();   // every warp is done with q and its ring
     if (more) begin(st);
@@ -589,24 +590,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
     auto o_at = [&](int w, int r) {
       return reinterpret_cast<float4 *>(smem + w * kRing + (st + C::AHEAD) % kStages * kStage + r * C::JOIN * 4);
     };
-    float f[2];   // O / l_warp * 2^{L_warp - L}, O being in units of 2^{M - shift - m}
+    // O's factor 2^{m_warp - m} 2^{M - shift - m_warp} / l as two, its power's root and
+    // the rest: a page of tiny V brings the power near float32's end, a distant
+    // maximum past it, where the whole product is not
+    float f0[2], f1[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = g + 8 * e;
       if (HALF && e) continue;
+      float2 ml[kWarps];
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * C::ROWS + r]);
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = stat[w * C::ROWS + r];
+        top = fmaxf(top, ml[w].x);
+      }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        sum += stat[w * C::ROWS + r] == -INFINITY ? 0.f : fast_exp2(stat[w * C::ROWS + r] - top);
-      f[e] = l[e] == 0.f ? 0.f
-                         : fast_exp2(m_d[e] - kShift) / l[e] *
-                               (fast_exp2(stat[warp * C::ROWS + r] - top) / sum);
+      for (int w = 0; w < kWarps; ++w) sum += ml[w].y == 0.f ? 0.f : fast_exp2(ml[w].x - top) * ml[w].y;
+      f0[e] = l[e] == 0.f ? 0.f : fast_exp2(0.5f * (m_s[e] - top + (m_d[e] - kShift)));
+      f1[e] = l[e] == 0.f ? 0.f : f0[e] / sum;
       if (warp == 0 && t == 0 && r < rows) {
-        const float L2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-        if (part < 0) p.lse[row0 + r] = L2 * 0.69314718055994531f;
-        else p.l_part[part + r] = L2;
+        if (part < 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        else p.l_part[part + r] = make_float2(top, sum);
       }
     }
 #pragma unroll
@@ -621,8 +626,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
         for (int i = 0; i < C::JOIN / 16; ++i) {
           const int c = half * (C::JOIN / 16) + i;
-          dst[4 * i] = make_float4(o[2 * c][2 * e] * f[e], o[2 * c + 1][2 * e] * f[e], o[2 * c][2 * e + 1] * f[e],
-                                   o[2 * c + 1][2 * e + 1] * f[e]);
+          dst[4 * i] = make_float4(o[2 * c][2 * e] * f1[e] * f0[e], o[2 * c + 1][2 * e] * f1[e] * f0[e],
+                                   o[2 * c][2 * e + 1] * f1[e] * f0[e], o[2 * c + 1][2 * e + 1] * f1[e] * f0[e]);
         }
       }
       __syncthreads();

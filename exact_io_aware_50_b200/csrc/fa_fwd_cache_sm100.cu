@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       // ------------------------------------------------------------ epilogue
       tc_fence_after();
       const bool seen = !(l == 0.f);
-      const float f = seen ? fast_exp2(m_d - kShift) / l : 0.f;
+      const float f0 = seen ? fast_exp2(0.5f * (m_d - kShift)) : 0.f, f1 = seen ? f0 / l : 0.f;   // as the rows kernel's
       const bool nans = nan_any[u & 1] != 0;
       const long long prt = x.part < 0 ? 0 : (long long)(x.part + t * BM + r);
 #pragma unroll 1
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         tmem_wait_ld();
         float *o = reinterpret_cast<float *>(ov);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = seen ? o[e] * f : 0.f;
+        for (int e = 0; e < 32; ++e) o[e] = seen ? o[e] * f1 * f0 : 0.f;
         if (nans) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
@@ -700,9 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         }
       }
       if (live) {
-        const float l2 = seen ? m_s + log2f(l) : -INFINITY;
-        if (x.part < 0) p.lse[row] = l2 * 0.69314718055994531f;
-        else p.l_part[prt] = l2;
+        if (x.part < 0) p.lse[row] = seen ? (m_s + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else p.l_part[prt] = make_float2(m_s, l);
       }
       tc_fence_before();
       mbar_arrive(bar(B_OEMPTY + t));

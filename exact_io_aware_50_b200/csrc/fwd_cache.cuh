@@ -35,7 +35,8 @@ struct FwdCacheParams {
   const int *table, *lens;
   __nv_bfloat16 *o;
   float *lse;
-  float *o_part, *l_part;   // [ctas][2][prows][D], [ctas][2][prows] (base 2)
+  float *o_part;            // [ctas][2][prows][D], normalised
+  float2 *l_part;           // [ctas][2][prows] (m, l): maximum (base 2) and sum
   int B, Hq, Hkv, Nq, g, R, tiles;   // R = g * Nq rows of a key/value head, in `tiles` tiles
   int page_log2, num_pages, max_pages;
   int causal, ctas, prows;   // prows: rows of a partial, min(R, rows of a tile)
@@ -323,7 +324,7 @@ constexpr int merge_ahead() { return W == 1 && L::QMAJOR ? 4 : 8; }
 // tile, the first of CTA c0; warp w of W.
 template <int D, class L, int W>
 __device__ __forceinline__ void merge_row(const FwdCacheParams &p, int row, int rr, int c0, int n, int warp, int lane,
-                                          float (*s_o)[D], float *s_w) {
+                                          float (*s_o)[D], float2 *s_w) {
   // piece i: the unit's start lies in the second slot of CTA c0, the rest in first ones
   auto at = [&](int i) { return ((long long)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.prows + rr; };
   constexpr int PER = D / 32, AHEAD = merge_ahead<L, W>();
@@ -334,18 +335,23 @@ __device__ __forceinline__ void merge_row(const FwdCacheParams &p, int row, int 
   for (int k = 0; k < AHEAD; ++k)
     if (warp + W * k < n) load_floats<PER>(src + at(warp + W * k) * D, v[k]);
   // lane i looks at pieces i, i + 32, ...
-  const float mine = lane < n ? p.l_part[at(lane)] : -INFINITY;
-  float top = mine;
-  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)]);
+  const float2 none = make_float2(-INFINITY, 0.f), mine = lane < n ? p.l_part[at(lane)] : none;
+  float top = mine.x;
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, p.l_part[at(i)].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const float own = mine == -INFINITY ? 0.f : fast_exp2(mine - top);   // weight of piece `lane`
-  float sum = own;
+  // a piece's weight 2^{m - top} l as two factors, the power's root and the rest: O of
+  // a page of large V may lie past float32's end where the product does not
+  auto weight = [&](const float2 &x) {
+    const float root = x.y == 0.f ? 0.f : fast_exp2(0.5f * (x.x - top));
+    return make_float2(root, x.y == 0.f ? 0.f : root * x.y);
+  };
+  const float2 own = weight(mine);   // of piece `lane`
+  float sum = own.x * own.y;
   if (W > 1 && lane < n && lane % W == warp) s_w[lane] = own;   // each warp keeps its own pieces' weights
   for (int i = lane + 32; i < n; i += 32) {
-    const float x = p.l_part[at(i)];
-    const float w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-    sum += w;
+    const float2 w = weight(p.l_part[at(i)]);
+    sum += w.x * w.y;
     if (W > 1 && i % W == warp) s_w[i] = w;
   }
 #pragma unroll
@@ -365,18 +371,16 @@ __device__ __forceinline__ void merge_row(const FwdCacheParams &p, int row, int 
     for (int k = 0; k < AHEAD; ++k)
       if (i0 + W * k < n) {
         const int i = i0 + W * k;
-        float w;
+        float2 w;
         if (W > 1) {
           w = s_w[i];
         } else {
-          w = __shfl_sync(0xffffffffu, own, i & 31);
-          if (i >= 32) {   // more pieces than lanes: the weight again
-            const float x = p.l_part[at(i)];
-            w = x == -INFINITY ? 0.f : fast_exp2(x - top);
-          }
+          w.x = __shfl_sync(0xffffffffu, own.x, i & 31);
+          w.y = __shfl_sync(0xffffffffu, own.y, i & 31);
+          if (i >= 32) w = weight(p.l_part[at(i)]);   // more pieces than lanes: the weight again
         }
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w.y, w.x * v[k][e], acc[e]);
       }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -406,7 +410,8 @@ __device__ __forceinline__ void merge_row(const FwdCacheParams &p, int row, int 
 
 template <int D, class L, int W>
 __global__ void __launch_bounds__(kMergeWarps * 32, merge_ahead<L, W>() == 8 ? 1 : D == 256 ? 3 : 4) fwd_cache_merge_kernel(const FwdCacheParams p, int each) {
-  __shared__ float s_o[W > 1 ? kMergeWarps : 1][D], s_w[kMaxCtas];
+  __shared__ float s_o[W > 1 ? kMergeWarps : 1][D];
+  __shared__ float2 s_w[kMaxCtas];
   __shared__ int s_unit[5];
   const int warp = W > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
   const int rows = p.B * p.Hq * p.Nq;   // < 2^31: the launcher checks
@@ -581,7 +586,7 @@ FwdCachePlan fwd_cache_tile_plan(const CacheArgs &a);
 int launch_fwd_cache_tiles(const CacheArgs &a, const FwdCachePlan &x);
 
 inline size_t fwd_cache_plan_bytes(const FwdCachePlan &x, int d) {
-  return x.whole ? 0 : (size_t)x.ctas * 2 * x.prows * (d + 1) * 4;
+  return x.whole ? 0 : (size_t)x.ctas * 2 * x.prows * (d + 2) * 4;
 }
 inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x) {
   FwdCacheParams p;
@@ -591,7 +596,7 @@ inline FwdCacheParams fwd_cache_params(const CacheArgs &a, const FwdCachePlan &x
   p.table = a.table; p.lens = a.lens;
   p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
   p.o_part = (float *)a.ws;
-  p.l_part = p.o_part + (size_t)x.ctas * 2 * x.prows * a.d;
+  p.l_part = (float2 *)(p.o_part + (size_t)x.ctas * 2 * x.prows * a.d);
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Nq = a.Nq; p.g = a.Hq / a.Hkv;
   p.g_inv = p.g == 1 ? 0 : ~0ull / p.g + 1;
   p.R = (int)x.R;

@@ -68,7 +68,8 @@ ROWS = [(1, 1), (4, 5), (1, 130)]    # query heads, queries: one row, two 16-row
 @pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("gap,first,others", [
-    (80, 0, 8000), (80, 0, 1e20), (20, 0, 1e30), (80, 1e-25, 1e10), (-80, 1e20, 0), (-80, 1e10, 1e-25)])
+    (80, 0, 8000), (80, 0, 1e20), (20, 0, 1e30), (80, 1e-25, 1e10), (-80, 1e20, 0), (-80, 1e10, 1e-25),
+    (88, 0, 8000), (96, 0, 8000), (88, 0, 1e20), (120, 0, 1e20), (88, 1e-25, 1e12), (120, 3e-30, 1e20), (-88, 1e20, 0)])
 def test_v_scales_far_apart(gap, first, others, d, rows):
     """The first page's keys score `gap` nats above the others; its V is of size
     `first`, the others' of size `others`.  Early causal queries see the first
@@ -138,3 +139,19 @@ def test_one_key_above_the_others(size, rows):
     for wide in (0, 4096):
         cache, table = cache_of(k, v, lens, page, wide)
         check(large_scores(max(size, 1e4), 3, Hq, Nq, d, g), cache, table, lens, page, False, 0.7, exact_scores=True)
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,wide", [(17, 0), (100, 0), (17, 4096), (1000, 4096), (3000, 8192)])
+def test_equal_keys_fall_apart_unevenly(n, wide, d, rows):
+    """Equal keys that warps and CTAs share unevenly are one mean all the same, whatever
+    the scores' size."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(d + Nq)
+    k = torch.zeros(1, 1, n, d)
+    k[..., 0] = 1.0
+    v = 1.0 + torch.randn(1, 1, n, d, generator=g)
+    cache, table = cache_of(k, v, [n], 16, wide)
+    for size in (1.0, 4e7, 1e9):
+        check(large_scores(size, 1, Hq, Nq, d, g), cache, table, [n], 16, False, 0.7, exact_scores=True)
