@@ -29,6 +29,16 @@ __device__ __forceinline__ float e4m3_block_scale(float amax) {
   return __uint_as_float((uint32_t)(max(k, -112) + 127) << 23);
 }
 
+// Whether a scale is a power of two, as every scale is that an append has chosen.
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0; }
+
+// The E4M3 code of x, rounded once: x is cut to float32 with its last bit set where
+// something was cut off, which no tie between two codes has.
+__device__ __forceinline__ uint32_t e4m3_code(double x) {
+  const float f = __double2float_rz(x);
+  return pack_e4m3x2((double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u), 0.f) & 0xFFu;
+}
+
 // Page number of a sequence's page-th page, or -1 when it is not in the cache.
 __device__ __forceinline__ int checked_page(const int *table, long long at, int num_pages,
                                             unsigned *err) {

@@ -3,9 +3,11 @@
 //
 // Writing: with amax the largest finite magnitude of the new values that fall
 // into a page, scale = 2^k, the least with amax <= 448 * 2^k, or the page's
-// older scale where that is larger; code = E4M3(x / scale).  Scales are powers
+// older scale where that is larger; code = E4M3(x / scale).  These scales are powers
 // of two, so dividing by one and growing one are exact but for codes that
-// leave E4M3's normal range.  Memory-bound: es bytes read and one written an
+// leave E4M3's normal range.  An older scale may be any other number (a cache that
+// something else filled): then quotients and products are taken in float64 and
+// rounded once, in loops of their own.  Memory-bound: es bytes read and one written an
 // element (es + 1 reading back); both kernels move 16 bytes of the wider side at
 // a time.
 //
@@ -36,6 +38,17 @@ struct Chunk {
     }
   }
 };
+
+// A CTA's n codes of x / s, and n codes of a page times r, in float64 (apart from the
+// kernel, whose registers they would take).
+template <class T>
+__device__ __noinline__ void encode_any(const T *x, uint8_t *codes, int n, float s) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) codes[i] = (uint8_t)e4m3_code((double)(float)x[i] / (double)s);
+}
+__device__ __noinline__ void grow_any(uint8_t *codes, int n, double r) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    codes[i] = (uint8_t)e4m3_code((double)e4m3x2_to_float2(codes[i]).x * r);
+}
 
 // One CTA per (touched page of a sequence, batch and head, K or V).  The new
 // tokens of a page lie together; each thread keeps its chunks of them in
@@ -92,7 +105,9 @@ __global__ void __launch_bounds__(CHUNKS == 8 ? 1024 : 512) cache_append_kernel(
   amax = 0.f;
   for (int w = 0; w < (int)blockDim.x / 32; ++w) amax = fmaxf(amax, s_red[w]);
   const float old = s_old, s = fmaxf(e4m3_block_scale(amax), old);
-  if (slot && s > old) {   // the older tokens' codes follow the scale
+  if (slot && s > old && !power_of_two(old)) {   // the older tokens' codes follow the scale
+    grow_any(dst, slot * a.d, (double)old / (double)s);
+  } else if (slot && s > old) {
     const float r = old / s;
     for (int i = threadIdx.x; i < slot * a.d / 16; i += blockDim.x) {
       uint4 v = reinterpret_cast<const uint4 *>(dst)[i];
@@ -105,7 +120,12 @@ __global__ void __launch_bounds__(CHUNKS == 8 ? 1024 : 512) cache_append_kernel(
       reinterpret_cast<uint4 *>(dst)[i] = v;
     }
   }
-  const float inv = 1.f / s;   // a power of two
+  if (threadIdx.x == 0) *scale = s;
+  if (!power_of_two(s)) {   // an older scale
+    encode_any(src, dst + slot * a.d, (hi - lo) * a.d, s);
+    return;
+  }
+  const float inv = 1.f / s;
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
     const int c = i * blockDim.x + threadIdx.x;
@@ -121,7 +141,6 @@ __global__ void __launch_bounds__(CHUNKS == 8 ? 1024 : 512) cache_append_kernel(
     if constexpr (N == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t *>(to) = w[0];
   }
-  if (threadIdx.x == 0) *scale = s;
 }
 
 // A thread takes 16 bytes of each output in `kReads` rows of one (b, h).

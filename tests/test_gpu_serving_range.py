@@ -1,5 +1,6 @@
 """Attention over the paged E4M3 cache at the ends of its range: pages whose V has
-very different scales, hidden ones among them; scores of any size.
+very different scales, hidden ones among them; scores of any size.  Appending to pages
+whose older scale is no power of two.
 
 Tolerances are those of test_gpu_serving.py (a weight rounded once to 11 bits, the
 scores' error e_s through the exponential, float32 sums, weights below 2^-26 of a row's
@@ -155,3 +156,58 @@ def test_equal_keys_fall_apart_unevenly(n, wide, d, rows):
     cache, table = cache_of(k, v, [n], 16, wide)
     for size in (1.0, 4e7, 1e9):
         check(large_scores(size, 1, Hq, Nq, d, g), cache, table, [n], 16, False, 0.7, exact_scores=True)
+
+
+CODES = e4m3_decode(np.arange(0x7F, dtype=np.uint8))
+TIES = (CODES[1:] + CODES[:-1]) / 2            # what lies between two codes, all on a float32
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("T", [6, 40])
+def test_append_to_pages_of_any_scale(dt, d, T):
+    """New tokens, multiples of an older scale that lie on a tie between two codes among
+    them, are rounded once; equal codes and scales."""
+    scales = [m / 128 for m in (41, 47, 51, 52, 55, 56, 60, 61, 63, 95, 104, 109, 112, 122, 127)] + [0.7, 1e-3, 3e7, 0.5]
+    scales = np.asarray(scales, np.float32)
+    H, page, start = len(scales), 64, 5
+    cache = new_cache(1, H, page, d)
+    cache[0].random_(0, 0x7F)
+    cache[1].random_(0x80, 0xFF)
+    cache[2][0] = cache[3][0] = torch.from_numpy(scales)
+    g = torch.Generator().manual_seed(d)
+    t = torch.from_numpy(TIES[TIES <= 224])
+    pick = t[torch.randint(len(t), (2, 1, H, T, d), generator=g)] * (1 - 2 * torch.randint(2, (2, 1, H, T, d), generator=g))
+    near = 1 + 2.0 ** -20 * torch.randint(-1, 2, pick.shape, generator=g)
+    k, v = (pick * near * torch.from_numpy(scales).double()[:, None, None]).to(dt)
+    ref, table = np_cache(cache), torch.tensor([[0]], dtype=torch.int32)
+    F.cache_append(k.cuda(), v.cuda(), *cache, table.cuda(), i32([start]))
+    torch.cuda.synchronize()
+    for x, i in ((k, 0), (v, 1)):
+        S.cache_append(f64(x), ref[i], ref[i + 2], table.tolist(), [start], None, page)
+        assert np.array_equal(ref[i + 2][0], scales)        # the older scales are the larger ones
+        assert np.array_equal(f64(cache[i + 2]), ref[i + 2])
+        assert np.array_equal(cache[i].cpu().numpy(), ref[i])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_grows_a_scale_that_is_no_power_of_two(d):
+    """Older codes times such a scale, next to a tie between two codes of the new one, are
+    rounded once."""
+    code = np.arange(0x31, 0x41)                            # 0.5625 to 2
+    tie = TIES[0x30:0x38]                                   # 0.53 to 0.97
+    scales = np.float32(tie[None, :] / CODES[code][:, None]).ravel()
+    scales = scales[(scales < 1) & (np.frexp(scales)[0] != 0.5)]
+    H, page = len(scales), 16
+    cache = new_cache(1, H, page, d)
+    for i in (0, 1):
+        cache[i][:] = torch.from_numpy(code.astype(np.uint8))[torch.arange(d) % 16] + 0x80 * i
+        cache[i + 2][0] = torch.from_numpy(scales)
+    x = torch.full((1, H, 2, d), 448.0)                     # the new scale: 1
+    ref, table = np_cache(cache), torch.tensor([[0]], dtype=torch.int32)
+    F.cache_append(x.cuda(), x.cuda(), *cache, table.cuda(), i32([9]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        S.cache_append(f64(x), ref[i], ref[i + 2], table.tolist(), [9], None, page)
+        assert (ref[i + 2] == 1).all() and np.array_equal(f64(cache[i + 2]), ref[i + 2])
+        assert np.array_equal(cache[i].cpu().numpy(), ref[i])
