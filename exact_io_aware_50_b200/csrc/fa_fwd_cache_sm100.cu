@@ -129,6 +129,63 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+// The running maximum m of a row's scores and the largest s - m + log2 sv of a block,
+// for scores so large that one rounding of s - m is off by whole units: s is rounded
+// once, by which equal scores stay equal, and the differences are exact.  The best of
+// s + log2 sv is kept as its two parts.
+__device__ __noinline__ float2 maxima_apart(uint32_t ts, const float2 *scs, float rc, float m, int lim) {
+  float best_s = -INFINITY, best_v = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    const float2 kv = scs[q];
+    const int seen = kv.y == -INFINITY ? 0 : lim - 16 * q;
+    uint32_t sq[16];
+    tmem_ld16(ts + 16 * q, sq);
+    tmem_wait_ld();
+    float mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, e < seen ? __uint_as_float(sq[e]) : -INFINITY);
+    mx = __fmul_rn(mx, fmaxf(rc * kv.x, kTiny));
+    m = fmaxf(m, mx);
+    if (mx - best_s + (kv.y - best_v) > 0.f) {
+      best_s = mx;
+      best_v = kv.y;
+    }
+  }
+  return make_float2(m, best_s - m + best_v);
+}
+
+// The weights of a block's 128 columns where they are not formed as products, and the
+// sum of the row's powers: 16 columns at a time.  Both are calls, apart from the
+// kernel's code, whose loops the rare path would lengthen (8192 square, Hq 32, Hkv 8, d
+// 128, causal: 748 us with them inline, 723 as calls).
+template <int CHUNK>
+__device__ __noinline__ float weigh_apart(uint32_t ts, uint32_t prow, const float2 *scs, float rc, float ms, float diff,
+                                          int lim, int r) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    const float2 kv = scs[q];
+    const float cf = fmaxf(rc * kv.x, kTiny), up = diff + kv.y;
+    const int seen = kv.y == -INFINITY ? 0 : lim - 16 * q;
+    uint32_t sq[16], pk[8];
+    tmem_ld16(ts + 16 * q, sq);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      // s rounded before m is subtracted: the largest gives 0, equal ones the same
+      const float x0 = e < seen ? __fmul_rn(__uint_as_float(sq[e]), cf) - ms : -INFINITY;
+      const float x1 = e + 1 < seen ? __fmul_rn(__uint_as_float(sq[e + 1]), cf) - ms : -INFINITY;
+      sum += fast_exp2(x0) + fast_exp2(x1);
+      pk[e / 2] = pack_half2(fast_exp2(x0 + up), fast_exp2(x1 + up));
+    }
+    const uint32_t at = prow + (q >> 2) * CHUNK + (((2 * (q & 3)) ^ (r & 7)) << 4);
+    st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
+    st_shared_v4(at ^ 16, pk[4], pk[5], pk[6], pk[7]);
+  }
+  return sum;
+}
+
 // 32 bytes, a whole sector, in one store.
 __device__ __forceinline__ void store8(void *dst, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]),
@@ -554,29 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           float ns = m_s == -INFINITY ? mxs : m_s + fmaxf(mxs, 0.f), top = mxo - (ns - m_0);
           big = __any_sync(0xffffffffu, fabsf(m_0) > kBig || (fabsf(ns) > kBig && ns != -INFINITY));
           if (big) {
-            // Scores so large that s - m above is off by whole units: s rounded once, by
-            // which equal scores stay equal, and exact differences.  The best of s +
-            // log2 sv is kept as its two parts.
-            float best_s = -INFINITY, best_v = 0.f;
-            ns = m_s;
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-              const float2 kv = scs[q];
-              const int seen = kv.y == -INFINITY ? 0 : lim - col0 - 16 * q;
-              uint32_t sq[16];
-              tmem_ld16(ts + 16 * q, sq);
-              tmem_wait_ld();
-              float mx = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) mx = fmaxf(mx, e < seen ? __uint_as_float(sq[e]) : -INFINITY);
-              mx = __fmul_rn(mx, fmaxf(rc * kv.x, kTiny));
-              ns = fmaxf(ns, mx);
-              if (mx - best_s + (kv.y - best_v) > 0.f) {
-                best_s = mx;
-                best_v = kv.y;
-              }
-            }
-            top = best_s - ns + best_v;
+            // Scores so large that s - m above is off by whole units: once more, exactly.
+            const float2 m = maxima_apart(ts, scs, rc, m_s, lim - col0);
+            ns = m.x;
+            top = m.y;
           }
           // a row that has seen no key yet has l = 0 and O = 0 (or nothing, block 0)
           const float shift = ns == m_s ? 0.f : m_s - ns, nd = fmaxf(shift + m_d, top);
@@ -588,42 +626,23 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
         const bool none = m_s == -INFINITY;
         const float ms = none ? 0.f : m_s, diff = none ? 0.f : kShift - m_d;
         float sum = 0.f;
-        if (g + j > 0) {                      // P V of the block before is done with P
-          ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
-          tc_fence_after();
-          if (!ok) break;
-        }
         const bool apart = __any_sync(0xffffffffu, diff + pages.top > kOver) || big;
-        if (apart) {                          // 16 columns at a time, small rather than fast
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
-            const float2 kv = scs[q];
-            const float cf = fmaxf(rc * kv.x, kTiny), up = diff + kv.y;
-            const int seen = kv.y == -INFINITY ? 0 : lim - col0 - 16 * q;
-            uint32_t sq[16], pk[8];
-            tmem_ld16(ts + 16 * q, sq);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              // s rounded before m is subtracted: the largest gives 0, equal ones the same
-              const float x0 = e < seen ? __fmul_rn(__uint_as_float(sq[e]), cf) - ms : -INFINITY;
-              const float x1 = e + 1 < seen ? __fmul_rn(__uint_as_float(sq[e + 1]), cf) - ms : -INFINITY;
-              sum += fast_exp2(x0) + fast_exp2(x1);
-              pk[e / 2] = pack_half2(fast_exp2(x0 + up), fast_exp2(x1 + up));
-            }
-            const uint32_t at = prow + (q >> 2) * C::CHUNK + (((2 * (q & 3)) ^ (r & 7)) << 4);
-            st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
-            st_shared_v4(at ^ 16, pk[4], pk[5], pk[6], pk[7]);
-          }
-          tc_fence_before();
-          mbar_arrive(bar(B_SEMPTY + t));
-        }
-#pragma unroll 1
-        for (int h = apart ? -1 : 1; h >= 0; --h) {
+        for (int h = 1; h >= 0; --h) {
           if (h == 0) {
             read_half(0);
             tc_fence_before();
             mbar_arrive(bar(B_SEMPTY + t));   // the next block's S may take the columns
+          } else if (g + j > 0) {             // P V of the block before is done with P
+            ok = warp_wait_all(bar(B_PEMPTY + t), (g + j - 1) & 1, wc);
+            tc_fence_after();
+            if (!ok) break;
+          }
+          if (apart) {                        // all of the block
+            sum = weigh_apart<C::CHUNK>(ts, prow, scs, rc, ms, diff, lim - col0, r);
+            tc_fence_before();
+            mbar_arrive(bar(B_SEMPTY + t));
+            break;
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {

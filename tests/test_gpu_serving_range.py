@@ -1,6 +1,7 @@
 """Attention over the paged E4M3 cache at the ends of its range: pages whose V has
-very different scales, hidden ones among them; scores of any size.  Appending to pages
-whose older scale is no power of two.
+very different scales, hidden ones among them; scores of any size; NaN, bad pages and
+empty batches there.  Appending to pages whose older scale is no power of two.  Calls
+that share buffers.
 
 Tolerances are those of test_gpu_serving.py (a weight rounded once to 11 bits, the
 scores' error e_s through the exponential, float32 sums, weights below 2^-26 of a row's
@@ -211,3 +212,112 @@ def test_append_grows_a_scale_that_is_no_power_of_two(d):
         S.cache_append(f64(x), ref[i], ref[i + 2], table.tolist(), [9], None, page)
         assert (ref[i + 2] == 1).all() and np.array_equal(f64(cache[i + 2]), ref[i + 2])
         assert np.array_equal(cache[i].cpu().numpy(), ref[i])
+
+
+# -------------------------------------------------- hidden, missing and empty
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("size,first", [(1.0, 0.0), (1e9, 1.0), (1e9, 0.0)])
+def test_masks_beside_far_scales_and_large_scores(size, first, rows):
+    """Causal rows, NaN codes behind each length, and a page that is none among pages of
+    large V, where weights are formed apart from the common path."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(Nq)
+    lens, page, d, n = [140, 300, 133], 16, 128, 300
+    k = torch.zeros(3, 1, n, d)
+    k[..., 0] = 1.0
+    v = torch.randn(3, 1, n, d, generator=g) * 1e4
+    v[:, :, :page] *= first
+    for wide in (0, 4096):
+        cache, table = cache_of(k, v, lens, page, wide)
+        table[0, 5] = table[1, 0] = -1
+        q = large_scores(size, 3, Hq, Nq, d, g)
+        q[..., 0] = q[..., 0].abs()
+        o, lse = F.forward_cache(q.cuda(), *cache, table.cuda(), i32(lens), scale=0.7)
+        assert F.fa_device_status() == F.FA_ERR_PAGE
+        ref_o, ref_l, w, _, unit = S.cache_attention(f64(q), *np_cache(cache), table.tolist(), lens, page, 0.7, True)
+        tol = np.abs(ref_o) * U16 + w * (2.0 ** -11 + 2.0 ** -13) + unit * 2.0 ** -37 + TINY
+        assert (np.abs(f64(o) - ref_o) <= tol).all()
+        assert np.array_equal(np.isneginf(f64(lse)), np.isneginf(ref_l))
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+@pytest.mark.parametrize("wide", [0, 4096])
+def test_nan_key_reaches_only_the_rows_that_see_it(wide, rows):
+    """A NaN code of K makes the rows that see its token NaN, O and L, and no others."""
+    Hq, Nq = rows
+    g = torch.Generator().manual_seed(3)
+    n, page, d = 260, 32, 64
+    k, v = torch.randn(2, 1, 1, n, d, generator=g)
+    cache, table = cache_of(k, v, [n], page, wide)
+    q = torch.randn(1, Hq, Nq, d, generator=g).to(torch.bfloat16).cuda()
+    ref = F.forward_cache(q, *cache, table.cuda(), i32([n]))
+    at = n - 1 - Nq // 2
+    cache[0][int(table[0, at // page]), 0, at % page, 7] = 0xFF
+    o, lse = F.forward_cache(q, *cache, table.cuda(), i32([n]))
+    torch.cuda.synchronize()
+    assert F.fa_device_status() == F.FA_OK
+    sees = torch.arange(Nq) + n - Nq >= at
+    assert torch.isnan(o[:, :, sees]).all() and torch.isnan(lse[:, :, sees]).all()
+    assert torch.equal(o[:, :, ~sees], ref[0][:, :, ~sees]) and torch.equal(lse[:, :, ~sees], ref[1][:, :, ~sees])
+
+
+@pytest.mark.parametrize("B", [1, 40, 200])
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: "x".join(map(str, r)))
+def test_batches_without_a_token(rows, B):
+    """Every sequence is empty: O = 0 and L = -inf all over, line or whole units."""
+    Hq, Nq = rows
+    for wide in (64, 8192):
+        cache = new_cache(3, 2, 16, 128)
+        table = torch.full((B, wide // 16), -1, dtype=torch.int32, device="cuda")
+        q = torch.randn(B, 2 * Hq, Nq, 128, device="cuda").to(torch.bfloat16)
+        o, lse = F.forward_cache(q, *cache, table, i32([0] * B))
+        torch.cuda.synchronize()
+        assert F.fa_device_status() == F.FA_OK
+        assert not o.any() and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------ shared buffers
+@pytest.mark.parametrize("Nq", [1, 200])
+def test_one_workspace_for_graphs_replayed_in_turn(Nq):
+    """Two captured calls on one caller's workspace, replayed one behind the other, whatever
+    the workspace held."""
+    g = torch.Generator().manual_seed(4)
+    n, page, d = 3000, 64, 64
+    need = F.fa_fwd_cache_workspace_size(1, 4, 2, Nq, d, page, -(-n // page))
+    work = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    calls = []
+    for _ in range(2):
+        k, v = torch.randn(2, 1, 2, n, d, generator=g)
+        cache, table = cache_of(k, v, [n], page)
+        calls.append((torch.randn(1, 4, Nq, d, generator=g).to(torch.bfloat16).cuda(), *cache, table.cuda(), i32([n])))
+    alone = [F.forward_cache(*c) for c in calls]
+    graphs = []
+    for c in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = F.forward_cache(*c, workspace=work)
+        graphs.append((graph, out))
+    for i in (0, 1, 1, 0, 1, 0):
+        for t in graphs[i][1]:
+            t.fill_(1.0)
+        graphs[i][0].replay()
+        graphs[1 - i][0].replay()
+        torch.cuda.synchronize()
+        for (_, out), ref in zip(graphs, alone):
+            assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+    assert F.fa_device_status() == F.FA_OK
+
+
+@pytest.mark.parametrize("rot", [32, 64, 128])
+def test_rope_with_one_tensor_in_place(rot):
+    """q turned where it stands, k into another tensor, and the other way round."""
+    q, k = (torch.randn(2, H, 33, 128, device="cuda").to(torch.bfloat16) for H in (4, 2))
+    freqs, ms = F.rope_freqs(rot)
+    pos = i32(list(range(33)))
+    want = F.rope(q, k, pos, freqs, ms)
+    for which in (0, 1):
+        a, b = q.clone(), k.clone()
+        out = (a, torch.empty_like(b)) if which == 0 else (torch.empty_like(a), b)
+        got = F.rope(a, b, pos, freqs, ms, out=out)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(b, k) if which == 0 else torch.equal(a, q)
