@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) fwd_cache_rows_kernel(const Fw
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += ml[w].y == 0.f ? 0.f : fast_exp2(ml[w].x - top) * ml[w].y;
       f0[e] = l[e] == 0.f ? 0.f : fast_exp2(0.5f * (m_s[e] - top + (m_d[e] - kShift)));
-      f1[e] = l[e] == 0.f ? 0.f : f0[e] / sum;
+      f1[e] = l[e] == 0.f ? 0.f : __fdividef(f0[e], sum);   // sum is below 2^32
       if (warp == 0 && t == 0 && r < rows) {
         if (part < 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
         else p.l_part[part + r] = make_float2(top, sum);
