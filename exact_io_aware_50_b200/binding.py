@@ -519,7 +519,10 @@ def rope_freqs(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=
                beta_fast=32.0, beta_slow=1.0, device="cuda"):
     """(freqs, mscale) for ``rope``: the float64 frequency table [rot_dim / 2]
     on `device` and the factor on the rotated values, scaled for long contexts
-    ("none", "linear", "ntk" or "yarn", fa_rope_freqs)."""
+    ("none", "linear", "ntk" or "yarn", fa_rope_freqs).  "yarn" blends by each
+    pair's turns within original_len, as its paper does; ``rope`` takes any
+    float64 table, so one that ramps over the pairs' indexes, as some
+    checkpoints' code does, is passed as it is."""
     import torch
     if scaling not in FA_ROPE_KINDS:
         raise ValueError(f"rope_freqs: scaling must be one of {tuple(FA_ROPE_KINDS)}")
@@ -615,8 +618,8 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, c
     """Write new tokens k, v [B, Hkv, T, d] (bfloat16 or float32) of each
     sequence at positions start[b] .. into the paged E4M3 cache, with one
     power-of-two scale per page and head (fa_cache_append).  count: int32 [B]
-    tokens of each sequence that count (None: all T).  The cache tensors are
-    updated in place."""
+    tokens of each sequence that count (None: all T).  A sequence whose start
+    is negative is left out.  The cache tensors are updated in place."""
     _t()
     shape, dtype = k.shape, k.dtype
     if (len(shape) != 4 or v.shape != shape or v.dtype is not dtype

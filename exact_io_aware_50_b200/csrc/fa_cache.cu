@@ -11,10 +11,14 @@
 // element (es + 1 reading back); both kernels move 16 bytes of the wider side at
 // a time.
 //
-// Measured on B200, bf16, Hkv 8, d 128, pages of 64: 4 x 4096 tokens written (82 MB)
-// 18.1 us = 4.5 TB/s, 69 % of a plain copy's rate: a CTA's stores wait for the maximum
-// over its page, so loads and stores overlap between CTAs only; 64 x 1 token 2.9 us,
-// a launch; 4 x 5001 to 8192 tokens read back (192 MB) 33.5 us = 5.7 TB/s, 87 %.
+// Measured on B200, bf16, Hkv 8, d 128, pages of 64: four prompts of 2048 to 4096 tokens
+// written (82 MB) 18.3 us = 4.5 TB/s, 69 % of a plain copy's rate, four of 4096 (101 MB)
+// 19.9 us = 5.1 TB/s; in float32 (168 MB) 27.7 us = 6.1 TB/s, 92 %.  In bf16 instructions
+// bound it as much as DRAM: 2.6 a cycle of four, about 17 an element, with 84 bytes
+// spilled (its 64 registers are those that 1024 threads may have, where a page of 64 x
+// 128 has 128); and a CTA's stores wait for the maximum over its page, so that loads and
+// stores overlap between CTAs only.  64 x 1 token 2.9 us, a launch; 4 x 5001 to 8192 tokens
+// read back (192 MB) 33.6 us = 5.7 TB/s, 87 %.
 #include "cache.cuh"
 
 namespace fa {

@@ -29,15 +29,17 @@
 // largest.  The weight that multiplies V is 2^{s - m} sv, rounded to a half.
 // It has a reference M of its own, the running maximum of s + log2 sv: terms
 // down to 2^-26 of the largest keep 11 bits whatever the pages' scales, and
-// smaller ones err by at most 2^-37 of the largest weight.
+// smaller ones err by at most 2^-37 of the largest weight.  M is kept as M - m, and
+// scores are subtracted before anything is added to them, so this holds for scores of
+// any size.
 //
 // Measured on B200, a call in a graph, Hq 32, Hkv 8, d 128: 32 sequences of 2047 to
 // 16384 tokens (612 MB) 98 us = 6.2 TB/s, 95 % of a plain copy's rate, the bound of
-// long batches; one of 16384 tokens 13.1 us, of which 7 are the latency of a call's
-// two launches, the page look-up, the first copies and the merge.  d = 256 holds O in
-// 128 registers a thread: B 8, Hq 16, Hkv 4, 16384 tokens 49 us = 5.5 TB/s.  Many
-// short sequences are bound by a unit's start and end, about 3.5 us of a CTA: 256 of
-// 256 tokens 39 us = 3.5 TB/s.  Copying the next unit's first steps before this one's
+// long batches (109 us = 5.6 TB/s called from Python); one of 16384 tokens 13.5 us, of
+// which 7 are the latency of a call's two launches, the page look-up, the first copies
+// and the merge.  d = 256 holds O in 128 registers a thread: B 8, Hq 16, Hkv 4, 16384
+// tokens 51 us = 5.3 TB/s.  Many short sequences are bound by a unit's start and end,
+// about 3.5 us of a CTA: 256 of 256 tokens 38 us = 3.5 TB/s.  Copying the next unit's first steps before this one's
 // last did not shorten that (2 to 5 % slower), nor did copies by TMA (boxes of 2 to 8
 // KB, one CTA an SM: 130 us for the batch where this form then took 109).
 #include <type_traits>
@@ -57,14 +59,16 @@ template <int D>
 struct RowCfg {
   static constexpr int ROWS = 16;
   // CTAs take whole units where the block table has room for this many tokens.
-  // Measured, us a call in a graph with the line and with whole units, Hkv 8, Hq 32:
-  // d = 64, 512 tokens, B 1 7.9 / 6.5, B 64 20.6 / 14.0; d = 128, 256 tokens 8.2 / 6.3
-  // and 16.6 / 13.2, 512 tokens 8.0 / 8.4 and 24.0 / 19.0 (and a launch less, 3 us of
-  // the host's time); d = 256, 256 tokens 9.0 / 9.0 and 25.4 / 20.7, 512 tokens 8.8 /
-  // 12.9 and 41.8 / 33.0.  With a unit for every CTA (B 64; B 50 ragged), d = 64, 2048
-  // tokens 31.4 / 29.9 and 25.7 / 25.7; d = 128, 1024 tokens 34.3 / 30.5 and 23.8 /
-  // 23.9, 2048 tokens 43.2 / 46.3 and 29.0 / 38.7; d = 256, 512 tokens 39.2 / 31.5 and
-  // 27.0 / 25.3, 1024 tokens 46.4 / 46.5 and 32.6 / 39.6.
+  // Measured, us a call in a graph with the line and with whole units, Hkv 8, Hq 32,
+  // one set of inputs: d = 64, 512 tokens, B 1 7.3 / 5.5, B 64 18.0 / 11.9; d = 128, 256
+  // tokens 7.3 / 5.1 and 14.6 / 11.1, 512 tokens 7.4 / 7.1 and 21.1 / 16.2 (and a launch
+  // less, 3 us of the host's time); d = 256, 256 tokens 8.1 / 7.8 and 22.9 / 18.5, 512
+  // tokens 7.8 / 11.5 and 37.4 / 30.2.  With a unit for every CTA (B 64; B 50 ragged; B
+  // 38, eight units more than CTAs, the worst: a second round for the eight), d = 64,
+  // 2048 tokens 37.2 / 33.5, 26.9 / 25.0 and 24.2 / 27.4; d = 128, 1024 tokens 33.0 /
+  // 29.3, 20.1 / 21.2 and 22.0 / 23.0, 2048 tokens 50.8 / 49.4, 27.8 / 36.7 and 34.6 /
+  // 43.1; d = 256, 512 tokens 37.5 / 30.2, 23.1 / 22.5 and 24.2 / 24.7, 1024 tokens 55.8 /
+  // 50.1, 32.0 / 37.6 and 38.0 / 43.3.
   static constexpr int WHOLE = D == 256 ? 256 : 512, WHOLE_MANY = D == 128 ? 1024 : D == 64 ? 2048 : 512;
   // A unit's start counts as four granules.  Measured, us a call in a graph
   // with 0 / 2 / 4 / 6: one sequence of 16384 tokens (Hq 32, Hkv 8, d 128) 16.3 /
@@ -665,12 +669,14 @@ int run_rows(const CacheArgs &a, const FwdCachePlan &x) {
 }
 
 // Up to three tiles of 16 rows (five at d = 64) go to the kernel of this file,
-// which reads the cache (L2, mostly) for each; more rows read it once for 128 of
-// them on tcgen05 (fa_fwd_cache_sm100.cu).  Measured on B200, us a call in a graph here
-// / there, B 32, 8000 tokens, 2 key/value heads: d = 64, 80 rows 77.0 / 89.9, 96 rows
-// 90.2 / 90.4; d = 128, 48 rows 72.3 / 83.1, 64 rows 90.8 / 83.8; d = 256, 48 rows 123 /
-// 143; B 1, 16000 tokens, 8 heads, 48 rows at d = 256 39.7 / 46.3; B 16, 400 tokens, 8
-// heads, 80 rows at d = 64 20.8 / 17.2, 40 rows at d = 256 27.8 / 21.7.
+// which reads the cache for each (a cache larger than L2 from DRAM each time: 48 rows
+// over 524 MB read 1579, 20 rows 1052, counted), converts and multiplies it anew; more
+// rows read it once for 128 of them on tcgen05 (fa_fwd_cache_sm100.cu).  Measured on
+// B200, us a call in a graph here / there, B 32, 8000 tokens, 2 key/value heads: d = 64,
+// 80 rows 78.4 / 82.7, 96 rows 92.3 / 83.0; d = 128, 48 rows 72.5 / 84.9, 64 rows 89.6 /
+// 85.1; d = 256, 48 rows 124 / 119; B 1, 16000 tokens, 8 heads, 48 rows at d = 256 39.9 /
+// 44.2; B 16, 400 tokens, 8 heads, 80 rows at d = 64 20.5 / 16.4, 40 rows at d = 256
+// 27.0 / 21.9.
 bool few_rows(const CacheArgs &a) {
   return (double)(a.Hq / a.Hkv) * a.Nq <= (a.d == 64 ? 5 : 3) * 16;
 }

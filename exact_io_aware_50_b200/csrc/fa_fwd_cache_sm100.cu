@@ -3,8 +3,8 @@
 // on tcgen05, TMEM accumulators.
 //
 // The mathematics are those of fa_fwd_cache.cu, with the same two references
-// (m for the sum of 2^{s - m}, M for the weights 2^{s - m} sv) and the same
-// roundings: q and the weights as halves, the codes exactly as halves.
+// (m for the sum of 2^{s - m}, M, kept as M - m, for the weights 2^{s - m} sv) and the
+// same roundings: q and the weights as halves, the codes exactly as halves.
 //
 // A CTA (one per SM, 16 warps) takes NT tiles of 128 rows of one key/value
 // head, row r being query r / g of the group's head r % g, and blocks of 128
@@ -24,12 +24,15 @@
 // the largest only.
 //
 // Measured on B200, a call: 512 queries over 16384 tokens, causal, Hq 8, Hkv 8, d 128,
-// 65 us = 520 TFLOP/s; 8192 square, Hq 32, 740 us = 743 TFLOP/s causal, 1273 us = 864
-// TFLOP/s not.  A block of 128 tokens takes about 5000 cycles for two tiles, of which
-// the tensor pipe's work is 2050 and the exponentials' 2050: the softmax's 4600 set
-// the pace, 72 % of the issue slots with the converters' instructions, and neither
-// removing the maxima, the exponentials or the conversion alone (timing copies)
-// shortened a call by more than 2 us.  Tried and slower: the weights in TMEM instead of
+// 63 us = 537 TFLOP/s; 8192 square, Hq 32, 717 us = 767 TFLOP/s causal, 1233 us = 892
+// TFLOP/s not; d = 256, Hq 16, Hkv 4, 4096 square causal, one tile a CTA, 246 us = 559.
+// A block of 128 tokens took about 5000 cycles for two tiles (clock stamps, calls then
+// 3 % slower), of which the tensor pipe's work is 2050 and the exponentials' 2050: the
+// softmax's 4600 set the pace, 72 % of the issue slots with the converters'
+// instructions, and neither removing the maxima, the exponentials or the conversion
+// alone (timing copies) shortened a call by more than 2 us.  The blocks are 35 us of the
+// first call; the rest is its start (9700 cycles to the first S), the partials' stores
+// (6000), the merge and the launches.  Tried and slower: the weights in TMEM instead of
 // shared memory, S of a block behind P V of the one before (68 us where this form
 // took 65), S read 32 columns at a time ahead of use (68), converters that sleep
 // between polls (67); pairs of float32 in one instruction changed nothing (65).
@@ -43,12 +46,13 @@ constexpr int kMmaWarp = 15;
 constexpr int kThreads = 512;
 // CTAs take whole units where the block table has room for this many tokens.
 // Measured, us a call in a graph with the line and with whole units, causal, d 128, Hkv
-// 8: B 1, Hq 8, 128 queries of 128 tokens 14.7 / 10.3, 512 of 512 22.3 / 22.3, 64 of 512
-// 14.7 / 16.3; B 1, Hq 32, 512 of 512 37.4 / 21.9; B 8, Hq 32, 128 of 128 31.1 / 14.6,
-// 512 of 512 119.6 / 65.8.  With a unit for every CTA, B 8, 512 of 2048 238 / 198 (ragged
-// 207 / 177), 512 of 4096 387 / 368 (ragged 277 / 328).
+// 8: B 1, Hq 8, 128 queries of 128 tokens 15.3 / 10.5, 512 of 512 22.7 / 22.2, 64 of 512
+// 15.1 / 16.3; B 1, Hq 32, 512 of 512 37.3 / 21.4; B 8, Hq 32, 128 of 128 31.6 / 14.5,
+// 512 of 512 107 / 64.6.  With a unit for every CTA, B 8, 512 of 2048 232 / 188 (ragged
+// 204 / 170), 512 of 4096 367 / 352 (ragged 266 / 314); B 19, 64 queries, four units more
+// than CTAs, 1024 tokens 71.6 / 59.3, 2048 tokens 98.0 / 101.1.
 constexpr int kWhole = 512, kWholeMany = 2048;
-constexpr float kBig = 1048576.f;               // scores past this are not subtracted in one rounding (half an ulp is 2^-4)
+constexpr float kBig = 1048576.f;               // past it, s - m in one rounding is off by 2^-4 and more
 constexpr float kTiny = 1.17549435e-38f;        // least factor of a score: a hidden -inf stays one
 
 template <int D_, int NT_>
@@ -360,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
             const float top = group_max<8>(lsv);
             hi = fmaxf(hi, top);
             lo = fminf(lo, -group_max<8>(lsv != -INFINITY ? -lsv : -INFINITY));
-            if (leader) block_pages[(g + j) & 3] = Pages{(there & 0xFFu) != 0xFFu, hi - lo > kOver - kShift ? top : -INFINITY};
+            if (leader)
+              block_pages[(g + j) & 3] = Pages{(there & 0xFFu) != 0xFFu, hi - lo > kOver - kShift ? top : -INFINITY};
           }
           store(C::OFF_K, kr);
           fence_proxy_async_smem();
@@ -687,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
       // ------------------------------------------------------------ epilogue
       tc_fence_after();
       const bool seen = !(l == 0.f);
-      const float f0 = seen ? fast_exp2(0.5f * (m_d - kShift)) : 0.f, f1 = seen ? f0 / l : 0.f;   // as the rows kernel's
+      // O's factor as two, as in the other kernel
+      const float f0 = seen ? fast_exp2(0.5f * (m_d - kShift)) : 0.f, f1 = seen ? f0 / l : 0.f;
       const bool nans = nan_any[u & 1] != 0;
       const long long prt = x.part < 0 ? 0 : (long long)(x.part + t * BM + r);
 #pragma unroll 1

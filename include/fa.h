@@ -352,7 +352,8 @@ int fa_rope_freqs(double *freqs, float *mscale, int rot_dim, double theta, int k
  * Page numbers are checked by the kernels: a token whose page number is
  * outside [0, num_pages), or whose place is outside the table's max_pages
  * pages, is left out (not written; read as zeros; hidden from every query),
- * a negative length counts as 0, and fa_device_status reports FA_ERR_PAGE.
+ * a negative length counts as 0, a negative start leaves out all of its
+ * sequence's new tokens, and fa_device_status reports FA_ERR_PAGE.
  *
  * fa_cache_append -- writes T new tokens of each sequence at positions
  * start[b] .. start[b] + n_b - 1, n_b = count ? min(count[b], T) : T (tokens
@@ -366,8 +367,10 @@ int fa_rope_freqs(double *freqs, float *mscale, int rot_dim, double theta, int k
  *             max(scale, need)    otherwise (the page holds older tokens),
  * and the older slots' codes become E4M3(code * old scale / new scale) when
  * the scale grows: by a power of two, so only codes that fall below 2^-6 are
- * rounded again.  New codes are E4M3(x / scale), round to nearest even;
- * infinities become +-448, NaN stays NaN.  Slots behind the last new token
+ * rounded again.  (An older scale that something else wrote may be any finite
+ * number above 0: every quotient and product is rounded once, to its code.)
+ * New codes are E4M3(x / scale), round to nearest even; infinities become
+ * +-448, NaN stays NaN.  Slots behind the last new token
  * keep their bytes.
  * No page may be written for two sequences, or twice, in one call (that page's
  * codes and scale are then undefined).  B * Hkv is at most 65535
@@ -407,8 +410,11 @@ int fa_cache_read_f32(const void *k_cache, const void *v_cache, const float *k_s
  * L = -inf.  Slots behind a sequence's length may hold anything.
  * Scores, the softmax statistics and O are float32; the codes enter the
  * matrix instructions exactly.  The weights exp(s - m) * v_scale are rounded
- * once to 11 bits, those below 2^-26 of a row's largest to steps of 2^-36 of it.
- * k_scale, v_scale: finite and > 0, as fa_cache_append writes them.
+ * once to 11 bits, those below 2^-26 of a row's largest to steps of 2^-36 of it,
+ * whatever the size of the scores and however far apart the pages' v_scale are.
+ * k_scale, v_scale: finite and > 0, as fa_cache_append writes them.  A score
+ * that leaves float32's range (and scale * max |q| * k_scale of a row and a page
+ * past 2^140) gives NaN or a row without keys.
  *
  * workspace: fa_fwd_cache_workspace_size(...) bytes, 256-byte aligned
  * (NULL when that is 0, as for tables of few tokens); contents ignored on entry and clobbered, so calls
