@@ -39,9 +39,10 @@
 // which 7 are the latency of a call's two launches, the page look-up, the first copies
 // and the merge.  d = 256 holds O in 128 registers a thread: B 8, Hq 16, Hkv 4, 16384
 // tokens 51 us = 5.3 TB/s.  Many short sequences are bound by a unit's start and end,
-// about 3.5 us of a CTA: 256 of 256 tokens 38 us = 3.5 TB/s.  Copying the next unit's first steps before this one's
-// last did not shorten that (2 to 5 % slower), nor did copies by TMA (boxes of 2 to 8
-// KB, one CTA an SM: 130 us for the batch where this form then took 109).
+// about 3.5 us of a CTA: 256 of 256 tokens 38 us = 3.5 TB/s.  Copying the next unit's
+// first steps before this one's last did not shorten that (2 to 5 % slower), nor did
+// copies by TMA (boxes of 2 to 8 KB, one CTA an SM: 130 us for the batch where this form
+// then took 109).
 #include <type_traits>
 
 #include "fwd_cache.cuh"

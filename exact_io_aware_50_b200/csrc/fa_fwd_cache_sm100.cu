@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_cache_tile_kernel(const FwdCa
           }
         }
         l = l * al + sum;
+        if (!ok) break;
         fence_proxy_async_smem();
         if (rescale && j > 0) {
 #pragma unroll 1
