@@ -1,6 +1,6 @@
 """Attention over the paged E4M3 cache at the ends of its range: pages whose V has
-very different scales, hidden ones among them; scores of any size; NaN, bad pages and
-empty batches there.  Appending to pages whose older scale is no power of two.  Calls
+very different scales, hidden ones among them, or the least one; scores of any size; NaN,
+bad pages and empty batches there.  Appending to pages whose older scale is no power of two.  Calls
 that share buffers.
 
 Tolerances are those of test_gpu_serving.py (a weight rounded once to 11 bits, the
@@ -321,3 +321,20 @@ def test_rope_with_one_tensor_in_place(rot):
         got = F.rope(a, b, pos, freqs, ms, out=out)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert torch.equal(b, k) if which == 0 else torch.equal(a, q)
+
+
+@pytest.mark.parametrize("B,Nq", [(300, 1), (148, 130)])
+def test_tiny_values_over_millions_of_tokens(B, Nq):
+    """V of the least scale there is, 2^-112, over 3 * 2^20 equal tokens, one page named again
+    and again: their mean is the value itself, though the sum's reciprocal times the scale
+    lies far below float32's normal numbers.  (Sums of equal powers of two are exact.)"""
+    page, d, n = 128, 64, 3 * 2 ** 20
+    cache = [torch.full((1, 1, page, d), c, dtype=torch.uint8, device="cuda") for c in (0, 0x38)]   # K 0, V 1
+    cache += [torch.ones(1, 1, device="cuda"), torch.full((1, 1), S.SCALE_MIN, device="cuda")]
+    table = torch.zeros(B, n // page, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, 1, Nq, d, device="cuda").to(torch.bfloat16)
+    o, lse = F.forward_cache(q, *cache, table, i32([n] * B), causal=False)
+    torch.cuda.synchronize()
+    assert F.fa_device_status() == F.FA_OK
+    assert float((o.double() / S.SCALE_MIN - 1).abs().max()) <= U16 + 2.0 ** -11
+    assert float((lse.double() - np.log(n)).abs().max()) <= 2.0 ** -18 * (1 + np.log(n))
